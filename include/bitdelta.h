@@ -311,6 +311,86 @@ bd_status bd_apply_q8(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in, 
                       const int32_t* user_ids, void* y, bd_dtype y_dtype, void* workspace,
                       size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- MX4 base weights */
+
+/* Microscaled 4-bit (MX4) weights and tokens, the MXFP4 format of the OCP
+ * Microscaling Formats specification v1.0, as a base under the deltas ([P2]
+ * "Production Engineering" 3, Quantized Base Model Compatibility, at 4.25 bits per
+ * weight).  A block of 32 consecutive columns of a row shares one scale 2^E, stored as
+ * the byte E + 127 (255: NaN); its elements are e2m1 codes: magnitude 0, 0.5, 1, 1.5, 2,
+ * 3, 4 or 6 for codes 0..7, negative with bit 3 set.
+ *  codes  : uint8 [rows][cols / 2], the lower column of a pair in the low nibble.
+ *  scales : uint8 [rows][bd_mx4_scale_stride(cols)], the bytes of cols / 32 blocks and
+ *           zeros up to the stride, a multiple of 16 (no padding when cols is a multiple
+ *           of 512).
+ * cols is a multiple of 64; codes and scales are 16-byte aligned. */
+
+/* Bytes of one row of scales: 16 ceil(cols / 512); 0 for invalid cols. */
+size_t bd_mx4_scale_stride(int64_t cols);
+
+/* Quantises w [rows][cols] (BD_F32 or BD_BF16; weights once at load, or a batch's
+ * tokens).  Per block, with a = max |w|: E = clamp(floor(log2 a) - 2, -127, 127) and
+ * each code is the one nearest to w / 2^E, ties to the even code, magnitudes above 6 to
+ * 6; a block of zeros gets byte 0.  A block holding a NaN or Inf gets byte 255 and codes
+ * 0, so that every product with it is NaN.  values_out (may be NULL, may be w itself):
+ * [rows][cols] of w's dtype, what the codes stand for, which is the W_base to compress
+ * a user's delta against.  rows == 0 is a no-op. */
+bd_status bd_quantize_mx4(const void* w, bd_dtype dtype, int64_t rows, int64_t cols,
+                          uint8_t* codes_out, uint8_t* scales_out, void* values_out,
+                          void* stream);
+
+/* out[o][i] = code 2^E of out_dtype (BD_F32 or BD_BF16; exact, Inf where the value is
+ * beyond the dtype's range, which no block quantised from finite values reaches). */
+bd_status bd_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                            int64_t cols, void* out, bd_dtype out_dtype, void* stream);
+
+/* Base products on MX4 rows of up to 4 matrices that read the same tokens:
+ * y[t][o] = sum_i x[t][i] code[o][i] 2^E, fp32 sums (overwrites y).
+ * bd_base_gemm_mx4_n takes bf16 tokens (BD_ERR_DTYPE otherwise); the weights are widened
+ * to bf16 exactly on chip.  bd_base_gemm_mx4x4_n takes MX4 tokens (bd_quantize_mx4 of
+ * x [T][d_in]); the products are exact in the block-scaled matrix instructions.
+ *  n_mats       : 1..4.   d_outs : host int64[n_mats].
+ *  w_codes, w_scales, ys : host arrays of n_mats device pointers; ys[i] fp32
+ *                 [T][d_outs[i]], 16-byte aligned.
+ *  workspace    : >= the query's bytes, 256-byte aligned, for the partial sums of a K
+ *                 that is split in ordered parts (small batches and matrices); NULL, or a
+ *                 query of 0: no split.  y repeats bit for bit from call to call either
+ *                 way; with and without a workspace it may differ by the order of its sums.
+ * T == 0 is a no-op; d_in is a multiple of 64; one operand is at most 2 GB. */
+size_t bd_base_gemm_mx4_n_workspace_bytes(int64_t T, int64_t d_in, int32_t n_mats,
+                                          const int64_t* d_outs);
+bd_status bd_base_gemm_mx4_n(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
+                             int32_t n_mats, const uint8_t* const* w_codes,
+                             const uint8_t* const* w_scales, const int64_t* d_outs,
+                             float* const* ys, void* workspace, size_t ws_bytes, void* stream);
+size_t bd_base_gemm_mx4x4_n_workspace_bytes(int64_t T, int64_t d_in, int32_t n_mats,
+                                            const int64_t* d_outs);
+bd_status bd_base_gemm_mx4x4_n(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T,
+                               int64_t d_in, int32_t n_mats, const uint8_t* const* w_codes,
+                               const uint8_t* const* w_scales, const int64_t* d_outs,
+                               float* const* ys, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* How bd_apply_mx4 takes the tokens into the base product: as they are, or quantised to
+ * MX4 within the call.  The delta product reads the bf16 tokens either way. */
+typedef enum { BD_MX4_TOKENS_BF16 = 0, BD_MX4_TOKENS_MX4 = 1 } bd_mx4_tokens;
+
+/* bd_apply with the base weight given as MX4 rows:
+ *     y[t] = base(X[t]) + scale_u (.) (X[t] . S_u^T),
+ * base as bd_base_gemm_mx4_n or bd_base_gemm_mx4x4_n (`tokens`).  bf16 X only
+ * (BD_ERR_UNSUPPORTED for fp32), up to 8192 tokens, any scale mode.
+ * workspace: >= bd_apply_mx4_workspace_bytes(...) bytes; other arguments, the status word
+ * and errors as for bd_apply. */
+size_t bd_apply_mx4_workspace_bytes(const bd_compress_params* p, int64_t T, int32_t n_users,
+                                    int64_t d_out, int64_t d_in, bd_dtype x_dtype,
+                                    bd_dtype y_dtype, bd_mx4_tokens tokens);
+bd_status bd_apply_mx4(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
+                       const uint8_t* w_codes, const uint8_t* w_scales, int64_t d_out,
+                       const uint64_t* signs_bank, const void* scales_bank,
+                       const bd_compress_params* p, int32_t n_users, const int32_t* user_ids,
+                       void* y, bd_dtype y_dtype, bd_mx4_tokens tokens, void* workspace,
+                       size_t ws_bytes, void* stream);
+
 /* Workspace of a prepared batch: the grouping of the tokens by user and, for
  * bf16 inputs, room for the tokens encoded as delta-product operands. */
 size_t bd_batch_workspace_bytes(int64_t T, int32_t n_users, int64_t d_in, bd_dtype x_dtype);

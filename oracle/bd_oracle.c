@@ -445,3 +445,69 @@ void orc_apply_q8(const void* x, int xdtype, int64_t T, int64_t d_in, const int8
         }
     }
 }
+
+/* ------------------------------------------------------------------ MX4 base
+ * Microscaled 4-bit weights and tokens (OCP Microscaling Formats v1.0, MXFP4): blocks of
+ * 32 consecutive columns of a row share one scale 2^E, stored as the byte E + 127 (255:
+ * NaN); an element is one e2m1 code, magnitude 0, .5, 1, 1.5, 2, 3, 4 or 6 (codes 0..7)
+ * and a sign (bit 3).  Two codes per byte, the lower column in the low nibble.  A row of
+ * scales is 16 ceil(cols / 512) bytes, zeros past cols / 32. */
+static const double k_e2m1[8] = {0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0};
+
+/* E = clamp(floor(log2 max|v|) - 2, -127, 127); the code nearest to |v| / 2^E, a tie to
+ * the even code, above 6 to 6.  A block of zeros: byte 0, codes 0.  A block holding a NaN or Inf: byte 255, codes 0. */
+void orc_mx4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                      uint8_t* scales) {
+    int64_t ld = 16 * ((cols + 511) / 512);
+    memset(codes, 0, (size_t)(rows * (cols / 2)));
+    memset(scales, 0, (size_t)(rows * ld));
+    for (int64_t o = 0; o < rows; ++o) {
+        for (int64_t b = 0; b < cols / 32; ++b) {
+            double a = 0.0;
+            int finite = 1;
+            for (int64_t i = 32 * b; i < 32 * b + 32; ++i) {
+                double v = (double)o_load(w, dtype, o * cols + i);
+                if (!isfinite(v)) finite = 0;
+                else if (fabs(v) > a) a = fabs(v);
+            }
+            if (!finite) {
+                scales[o * ld + b] = 255;
+                continue;
+            }
+            int e = -127;
+            if (a > 0.0) {
+                frexp(a, &e); /* a = m 2^e, m in [0.5, 1) */
+                e -= 3;
+                if (e < -127) e = -127;
+                if (e > 127) e = 127;
+            }
+            scales[o * ld + b] = (uint8_t)(e + 127);
+            for (int64_t i = 32 * b; i < 32 * b + 32; ++i) {
+                double v = (double)o_load(w, dtype, o * cols + i);
+                double r = ldexp(fabs(v), -e);
+                int best = 0;
+                for (int c = 1; c < 8; ++c) {
+                    double d = fabs(r - k_e2m1[c]), db = fabs(r - k_e2m1[best]);
+                    if (d < db || (d == db && (c & 1) == 0)) best = c;
+                }
+                if (signbit(v)) best |= 8;
+                codes[o * (cols / 2) + i / 2] |= (uint8_t)(best << (4 * (i & 1)));
+            }
+        }
+    }
+}
+
+/* out[o][i] = code * 2^(byte - 127) in binary64 (byte 255: NaN). */
+void orc_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                        double* out) {
+    int64_t ld = 16 * ((cols + 511) / 512);
+    for (int64_t o = 0; o < rows; ++o) {
+        for (int64_t i = 0; i < cols; ++i) {
+            int c = (codes[o * (cols / 2) + i / 2] >> (4 * (i & 1))) & 15;
+            int s = scales[o * ld + i / 32];
+            double m = k_e2m1[c & 7];
+            if (c & 8) m = -m;
+            out[o * cols + i] = s == 255 ? NAN : ldexp(m, s - 127);
+        }
+    }
+}

@@ -66,6 +66,10 @@ def lib():
         L.orc_compress.restype = i64
         L.orc_select_axis.argtypes = [vp, vp, i32, i64, i64, dbl, vp]
         L.orc_select_axis.restype = i64
+        L.orc_mx4_quantize.argtypes = [vp, i32, i64, i64, vp, vp]
+        L.orc_mx4_quantize.restype = None
+        L.orc_mx4_dequantize.argtypes = [vp, vp, i64, i64, vp]
+        L.orc_mx4_dequantize.restype = None
         L.orc_quantize_rows.argtypes = [vp, i32, i64, i64, vp, vp]
         L.orc_quantize_rows.restype = None
         L.orc_apply_q8.argtypes = [vp, i32, i64, i64, vp, vp, i64, vp, vp, i32, i64, i32, i32,
@@ -199,6 +203,27 @@ def apply_q8(x: np.ndarray, q: np.ndarray, s: np.ndarray, words_bank: np.ndarray
     lib().orc_apply_q8(_p(x), _dtype_of(x, xdtype), T, d_in, _p(q), _p(s), n_rows, _p(words_bank),
                        _p(scales_bank), mode, g, sdtype, U, _p(ids), _p(y), _p(yb), _p(yd))
     return y, yb, yd
+
+
+def mx4_quantize(w: np.ndarray, dtype=None):
+    """MX4 rows (32-column blocks of e2m1 codes under one power-of-two scale byte):
+    returns (codes uint8 [rows][cols / 2], scales uint8 [rows][16 ceil(cols / 512)])."""
+    w = np.ascontiguousarray(w)
+    rows, cols = w.shape
+    codes = np.zeros((rows, cols // 2), dtype=np.uint8)
+    scales = np.zeros((rows, 16 * ((cols + 511) // 512)), dtype=np.uint8)
+    lib().orc_mx4_quantize(_p(w), _dtype_of(w, dtype), rows, cols, _p(codes), _p(scales))
+    return codes, scales
+
+
+def mx4_dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """The values MX4 rows stand for, in binary64."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    scales = np.ascontiguousarray(scales, dtype=np.uint8)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    out = np.empty((rows, cols), dtype=np.float64)
+    lib().orc_mx4_dequantize(_p(codes), _p(scales), rows, cols, _p(out))
+    return out
 
 
 def select_axis(wf: np.ndarray, wb, clip_k: float = 0.0, dtype=None):

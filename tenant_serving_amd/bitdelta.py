@@ -24,6 +24,8 @@ BD_OK, BD_ERR_INVALID_ARG, BD_ERR_SHAPE, BD_ERR_DTYPE, BD_ERR_UNSUPPORTED = 0, 1
 BD_ERR_WORKSPACE, BD_ERR_DEVICE, BD_ERR_NONFINITE, BD_ERR_USER_ID, BD_ERR_BATCH = 5, 6, 7, 8, 9
 BD_F32, BD_BF16, BD_F16 = 0, 1, 2
 BD_SCALE_MATRIX, BD_SCALE_GROUP, BD_SCALE_ROW, BD_SCALE_COL = 0, 1, 2, 3
+BD_MX4_TOKENS_BF16, BD_MX4_TOKENS_MX4 = 0, 1
+MX4_TOKENS = {"bf16": BD_MX4_TOKENS_BF16, "mx4": BD_MX4_TOKENS_MX4}
 MODE_NAMES = {"matrix": BD_SCALE_MATRIX, "group": BD_SCALE_GROUP, "row": BD_SCALE_ROW,
               "col": BD_SCALE_COL}
 
@@ -125,6 +127,26 @@ def lib() -> ctypes.CDLL:
         L.bd_decode_apply.restype = ctypes.c_int
         L.bd_decode_apply.argtypes = [vp, ctypes.c_int, i64, i64, vp, i64, vp, vp, P, i32, vp,
                                       ctypes.c_int, vp, sz, vp]
+        L.bd_mx4_scale_stride.restype = sz
+        L.bd_mx4_scale_stride.argtypes = [i64]
+        L.bd_quantize_mx4.restype = ctypes.c_int
+        L.bd_quantize_mx4.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp, vp, vp]
+        L.bd_dequantize_mx4.restype = ctypes.c_int
+        L.bd_dequantize_mx4.argtypes = [vp, vp, i64, i64, vp, ctypes.c_int, vp]
+        for f in (L.bd_base_gemm_mx4_n_workspace_bytes, L.bd_base_gemm_mx4x4_n_workspace_bytes):
+            f.restype = sz
+            f.argtypes = [i64, i64, i32, vp]
+        L.bd_base_gemm_mx4_n.restype = ctypes.c_int
+        L.bd_base_gemm_mx4_n.argtypes = [vp, ctypes.c_int, i64, i64, i32, vp, vp, vp, vp, vp, sz,
+                                         vp]
+        L.bd_base_gemm_mx4x4_n.restype = ctypes.c_int
+        L.bd_base_gemm_mx4x4_n.argtypes = [vp, vp, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.bd_apply_mx4_workspace_bytes.restype = sz
+        L.bd_apply_mx4_workspace_bytes.argtypes = [P, i64, i32, i64, i64, ctypes.c_int,
+                                                   ctypes.c_int, ctypes.c_int]
+        L.bd_apply_mx4.restype = ctypes.c_int
+        L.bd_apply_mx4.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp, i64, vp, vp, P, i32, vp, vp,
+                                   ctypes.c_int, ctypes.c_int, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -609,6 +631,186 @@ def apply_q8(x, wq, wscales, signs_bank, scales_bank, p, user_ids, y_dtype=torch
            "bd_apply_q8")
     if check:
         _check(bd_device_status(ws, stream), "bd_apply_q8 (device)")
+    return y
+
+
+# -------------------------------------------------------- MX4 base weights
+# (a matrix [rows][cols] is codes uint8 [rows][cols // 2] and scales uint8
+# [rows][bd_mx4_scale_stride(cols)]; see include/bitdelta.h)
+
+def bd_mx4_scale_stride(cols: int) -> int:
+    return int(lib().bd_mx4_scale_stride(int(cols)))
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device as the current one for the launches of a call."""
+    return torch.cuda.device(t.device)
+
+
+def _mx4(codes, scales, name: str, device=None, cols: Optional[int] = None):
+    """(rows, cols) of an MX4 matrix after the checks of its two tensors."""
+    if isinstance(codes, torch.Tensor) and (
+            codes.dim() != 2 or (cols is not None and 2 * codes.shape[1] != cols)):
+        raise ValueError(f"{name} codes have shape {tuple(codes.shape)}, expected (rows, "
+                         f"{'cols' if cols is None else cols} / 2)")
+    _dev(codes, name + " codes", (torch.uint8,), None, device)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    _dev(scales, name + " scales", (torch.uint8,), (rows, 16 * ((cols + 511) // 512)),
+         codes.device)
+    return rows, cols
+
+
+def bd_quantize_mx4(w, codes_out, scales_out, values_out=None, stream=None) -> int:
+    _dev(w, "w", (torch.float32, torch.bfloat16))
+    if w.dim() != 2:
+        raise ValueError("w must be two-dimensional")
+    rows, cols = w.shape
+    _dev(codes_out, "codes_out", (torch.uint8,), (rows, cols // 2), w.device)
+    _dev(scales_out, "scales_out", (torch.uint8,), (rows, 16 * ((cols + 511) // 512)), w.device)
+    _dev(values_out, "values_out", (w.dtype,), (rows, cols), w.device, optional=True)
+    with _on(w):
+        return int(lib().bd_quantize_mx4(_ptr(w), _dtype_code(w), rows, cols, _ptr(codes_out),
+                                         _ptr(scales_out), _ptr(values_out), _stream(w, stream)))
+
+
+def bd_dequantize_mx4(codes, scales, out, stream=None) -> int:
+    rows, cols = _mx4(codes, scales, "base")
+    _dev(out, "out", (torch.float32, torch.bfloat16), (rows, cols), codes.device)
+    with _on(out):
+        return int(lib().bd_dequantize_mx4(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
+                                           _dtype_code(out), _stream(out, stream)))
+
+
+def _mx4_mats(T, d_in, bases, ys, workspace, device):
+    if not 1 <= len(bases) <= 4 or len(ys) != len(bases):
+        raise ValueError("1..4 matrices, one output each")
+    for (codes, scales), y in zip(bases, ys):
+        rows, _ = _mx4(codes, scales, "base", device, d_in)
+        _dev(y, "y", (torch.float32,), (T, rows), device)
+    _dev(workspace, "workspace", None, None, device, optional=True)
+    return (len(ys), _ptr_array([c for c, _ in bases]), _ptr_array([s for _, s in bases]),
+            (ctypes.c_int64 * len(ys))(*[c.shape[0] for c, _ in bases]), _ptr_array(ys),
+            _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+
+
+def bd_base_gemm_mx4_n_workspace_bytes(T: int, d_in: int, d_outs) -> int:
+    arr = (ctypes.c_int64 * len(d_outs))(*[int(d) for d in d_outs])
+    return int(lib().bd_base_gemm_mx4_n_workspace_bytes(T, d_in, len(d_outs), arr))
+
+
+def bd_base_gemm_mx4_n(x, bases, ys, workspace=None, stream=None) -> int:
+    """Base products of bf16 tokens with up to 4 MX4 matrices; bases: (codes, scales) of
+    each, ys: fp32 outputs, `workspace` sized by the query (None: no split of K)."""
+    _dev(x, "x", (torch.bfloat16,))
+    T, d_in = x.shape
+    args = _mx4_mats(T, d_in, bases, ys, workspace, x.device)
+    with _on(x):
+        return int(lib().bd_base_gemm_mx4_n(_ptr(x), BD_BF16, T, d_in, *args, _stream(x, stream)))
+
+
+def bd_base_gemm_mx4x4_n_workspace_bytes(T: int, d_in: int, d_outs) -> int:
+    arr = (ctypes.c_int64 * len(d_outs))(*[int(d) for d in d_outs])
+    return int(lib().bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, len(d_outs), arr))
+
+
+def bd_base_gemm_mx4x4_n(x_codes, x_scales, bases, ys, workspace=None, stream=None) -> int:
+    """bd_base_gemm_mx4_n on MX4 tokens (codes and scales of bd_quantize_mx4)."""
+    T, d_in = _mx4(x_codes, x_scales, "token")
+    args = _mx4_mats(T, d_in, bases, ys, workspace, x_codes.device)
+    with _on(x_codes):
+        return int(lib().bd_base_gemm_mx4x4_n(_ptr(x_codes), _ptr(x_scales), T, d_in, *args,
+                                              _stream(x_codes, stream)))
+
+
+def bd_apply_mx4_workspace_bytes(p, T: int, n_users: int, d_out: int, d_in: int, x_dtype: int,
+                                 y_dtype: int, tokens="bf16") -> int:
+    return int(lib().bd_apply_mx4_workspace_bytes(ctypes.byref(p), T, n_users, d_out, d_in,
+                                                  x_dtype, y_dtype, _tokens(tokens)))
+
+
+def _tokens(tokens) -> int:
+    if isinstance(tokens, str):
+        if tokens not in MX4_TOKENS:
+            raise ValueError(f"tokens is {tokens!r}, expected one of {sorted(MX4_TOKENS)}")
+        return MX4_TOKENS[tokens]
+    return int(tokens)
+
+
+def bd_apply_mx4(x, codes, scales, signs_bank, scales_bank, p, n_users, user_ids, y, workspace,
+                 tokens="bf16", stream=None) -> int:
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    T, d_in = x.shape
+    dev = x.device
+    d_out, _ = _mx4(codes, scales, "base", dev, d_in)
+    _bank(signs_bank, scales_bank, p, n_users, d_out, d_in, dev)
+    _ids(user_ids, T, dev)
+    _dev(y, "y", (torch.float32, torch.bfloat16), (T, d_out), dev)
+    _dev(workspace, "workspace", None, None, dev)
+    with _on(x):
+        return int(lib().bd_apply_mx4(_ptr(x), _dtype_code(x), T, d_in, _ptr(codes), _ptr(scales),
+                                      d_out, _ptr(signs_bank), _ptr(scales_bank), ctypes.byref(p),
+                                      int(n_users), _ptr(user_ids), _ptr(y), _dtype_code(y),
+                                      _tokens(tokens), _ptr(workspace), _nbytes(workspace),
+                                      _stream(x, stream)))
+
+
+def quantize_mx4(w: torch.Tensor, values: bool = False, stream=None):
+    """(codes, scales) of w in MX4, and with `values` also what they stand for, in w's
+    dtype (bd_quantize_mx4)."""
+    rows, cols = w.shape
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((rows, 16 * ((cols + 511) // 512)), dtype=torch.uint8, device=w.device)
+    out = torch.empty_like(w) if values else None
+    _check(bd_quantize_mx4(w, codes, scales, out, stream), "bd_quantize_mx4")
+    return (codes, scales, out) if values else (codes, scales)
+
+
+def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bfloat16,
+                   stream=None) -> torch.Tensor:
+    out = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=out_dtype, device=codes.device)
+    _check(bd_dequantize_mx4(codes, scales, out, stream), "bd_dequantize_mx4")
+    return out
+
+
+def base_gemm_mx4(x: torch.Tensor, bases, ws=None, stream=None):
+    """[x . W^T] in fp32 for 1..4 MX4 matrices (codes, scales) and bf16 tokens x."""
+    T, d_in = x.shape
+    outs = [c.shape[0] for c, _ in bases]
+    ys = [torch.empty((T, n), dtype=torch.float32, device=x.device) for n in outs]
+    if ws is None:
+        need = bd_base_gemm_mx4_n_workspace_bytes(T, d_in, outs)
+        ws = workspace(need, x.device) if need > 0 else None
+    _check(bd_base_gemm_mx4_n(x, bases, ys, ws, stream), "bd_base_gemm_mx4_n")
+    return ys
+
+
+def base_gemm_mx4x4(xq, bases, ws=None, stream=None):
+    """base_gemm_mx4 on MX4 tokens xq = (codes, scales)."""
+    x_codes, x_scales = xq
+    T, d_in = x_codes.shape[0], 2 * x_codes.shape[1]
+    outs = [c.shape[0] for c, _ in bases]
+    ys = [torch.empty((T, n), dtype=torch.float32, device=x_codes.device) for n in outs]
+    if ws is None:
+        need = bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, outs)
+        ws = workspace(need, x_codes.device) if need > 0 else None
+    _check(bd_base_gemm_mx4x4_n(x_codes, x_scales, bases, ys, ws, stream), "bd_base_gemm_mx4x4_n")
+    return ys
+
+
+def apply_mx4(x, codes, scales, signs_bank, scales_bank, p, user_ids, y_dtype=torch.float32,
+              tokens="bf16", ws=None, stream=None, check: bool = False) -> torch.Tensor:
+    """bd_apply on an MX4 base (codes, scales); tokens: how the base product reads x,
+    "bf16" as it is or "mx4" quantised within the call."""
+    T, d_in = x.shape
+    d_out, U = codes.shape[0], signs_bank.shape[0]
+    y = torch.empty((T, d_out), dtype=y_dtype, device=x.device)
+    if ws is None:
+        ws = workspace(bd_apply_mx4_workspace_bytes(p, T, U, d_out, d_in, _dtype_code(x),
+                                                    _dtype_code(y), tokens), x.device)
+    _check(bd_apply_mx4(x, codes, scales, signs_bank, scales_bank, p, U, user_ids, y, ws, tokens,
+                        stream), "bd_apply_mx4")
+    if check:
+        _check(bd_device_status(ws, stream), "bd_apply_mx4 (device)")
     return y
 
 

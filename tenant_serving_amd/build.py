@@ -28,7 +28,7 @@ HIP_FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",
              "-I" + INCLUDE, "-I" + CSRC]
 
 BITDELTA_SOURCES = ["bd_api.hip", "bd_compress.hip", "bd_apply.hip", "bd_decode.hip", "bd_delta.hip", "bd_gemm.hip",
-                    "bd_reconstruct.hip"]
+                    "bd_mx4.hip", "bd_reconstruct.hip"]
 
 
 def _run(cmd, verbose):

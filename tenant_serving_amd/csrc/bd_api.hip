@@ -16,6 +16,8 @@ static __device__ __align__(256) char scratch[BD_NOALLOC_SCRATCH_BYTES];
 namespace {
 
 bool valid_wdtype(int d) { return d == BD_F32 || d == BD_BF16; }
+// largest MX4 matrix bd_quantize_mx4 takes
+constexpr int64_t kMx4MaxCols = (int64_t)1 << 31, kMx4MaxRows = ((int64_t)1 << 31) - 1;
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Device address of `scratch` on the current device (looked up on the first call per
@@ -435,6 +437,172 @@ bd_status bd_apply_q8(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in, 
     if (e == hipSuccess) e = launch_gemm_q8(x, T, d_in, wq, wscales, d_out, yacc, s);
     if (e == hipSuccess)
         e = launch_delta(pl.batch, pl.delta, ws, x, signs_bank, scales_bank, yacc, s);
+    if (e == hipSuccess && y_dtype == BD_BF16)
+        e = launch_cast_bf16(yacc, (uint16_t*)y, T * d_out, s);
+    return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+}
+
+size_t bd_mx4_scale_stride(int64_t cols) {
+    return cols > 0 && cols % 64 == 0 ? (size_t)mx4_scale_stride(cols) : 0;
+}
+
+bd_status bd_quantize_mx4(const void* w, bd_dtype dtype, int64_t rows, int64_t cols,
+                          uint8_t* codes_out, uint8_t* scales_out, void* values_out,
+                          void* stream) {
+    if (!valid_wdtype(dtype)) return BD_ERR_DTYPE;
+    if (rows < 0) return BD_ERR_INVALID_ARG;
+    if (cols <= 0 || cols % 64 != 0 || cols > kMx4MaxCols || rows > kMx4MaxRows) return BD_ERR_SHAPE;
+    if (rows == 0) return BD_OK;
+    if (!w || !codes_out || !scales_out || !aligned(w, 16) || !aligned(codes_out, 16) ||
+        !aligned(scales_out, 16) || (values_out && !aligned(values_out, 16)))
+        return BD_ERR_INVALID_ARG;
+    hipError_t e = launch_mx4_quantize(w, dtype, rows, cols, codes_out, scales_out, values_out,
+                                       (hipStream_t)stream);
+    return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+}
+
+bd_status bd_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                            int64_t cols, void* out, bd_dtype out_dtype, void* stream) {
+    if (!valid_wdtype(out_dtype)) return BD_ERR_DTYPE;
+    if (rows < 0) return BD_ERR_INVALID_ARG;
+    if (cols <= 0 || cols % 64 != 0 || cols > kMx4MaxCols || rows > kMx4MaxRows) return BD_ERR_SHAPE;
+    if (rows == 0) return BD_OK;
+    if (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16))
+        return BD_ERR_INVALID_ARG;
+    hipError_t e = launch_mx4_dequantize(codes, scales, rows, cols, out, out_dtype, (hipStream_t)stream);
+    return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+}
+
+static size_t mx4_n_workspace_bytes(bool x4, int64_t T, int64_t d_in, int32_t n_mats,
+                                    const int64_t* d_outs) {
+    if (T <= 0 || n_mats < 1 || n_mats > kMaxMats || !d_outs || d_in <= 0) return 0;
+    for (int i = 0; i < n_mats; ++i)
+        if (d_outs[i] <= 0 || !mx4_product_supported(x4, T, d_in, d_outs[i])) return 0;
+    return mx4_product_bytes(x4, T, d_in, d_outs, n_mats);
+}
+
+// x_scales: the tokens' scale bytes (MX4 tokens), or null (bf16 tokens).
+static bd_status base_gemm_mx4(const void* x, const uint8_t* x_scales, bool x4, int64_t T,
+                               int64_t d_in, int32_t n_mats, const uint8_t* const* w_codes,
+                               const uint8_t* const* w_scales, const int64_t* d_outs,
+                               float* const* ys, void* workspace, size_t ws_bytes, void* stream) {
+    if (T < 0 || n_mats < 1 || n_mats > kMaxMats || !w_codes || !w_scales || !d_outs || !ys)
+        return BD_ERR_INVALID_ARG;
+    if (d_in <= 0 || d_in % 64 != 0) return BD_ERR_SHAPE;
+    for (int i = 0; i < n_mats; ++i) {
+        if (d_outs[i] <= 0) return BD_ERR_SHAPE;
+        if (!mx4_product_supported(x4, T, d_in, d_outs[i])) return BD_ERR_UNSUPPORTED;
+    }
+    if (T == 0) return BD_OK;
+    if (!x || !aligned(x, 16) || (x4 && (!x_scales || !aligned(x_scales, 16)))) return BD_ERR_INVALID_ARG;
+    GemmMatArg m[kMaxMats];
+    for (int i = 0; i < n_mats; ++i) {
+        if (!w_codes[i] || !w_scales[i] || !ys[i] || !aligned(w_codes[i], 16) ||
+            !aligned(w_scales[i], 16) || !aligned(ys[i], 16))
+            return BD_ERR_INVALID_ARG;
+        m[i] = GemmMatArg{w_codes[i], ys[i], d_outs[i]};
+    }
+    const size_t need = mx4_product_bytes(x4, T, d_in, d_outs, n_mats);
+    char* ws = need > 0 ? (char*)workspace : nullptr;
+    if (ws && (ws_bytes < need || !aligned(ws, kAlign))) return BD_ERR_WORKSPACE;
+    hipError_t e = launch_mx4_product(x, x4 ? x_scales : nullptr, T, d_in, m, w_scales, n_mats, ws,
+                                      (hipStream_t)stream);
+    return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+}
+
+size_t bd_base_gemm_mx4_n_workspace_bytes(int64_t T, int64_t d_in, int32_t n_mats,
+                                          const int64_t* d_outs) {
+    return mx4_n_workspace_bytes(false, T, d_in, n_mats, d_outs);
+}
+
+bd_status bd_base_gemm_mx4_n(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
+                             int32_t n_mats, const uint8_t* const* w_codes,
+                             const uint8_t* const* w_scales, const int64_t* d_outs,
+                             float* const* ys, void* workspace, size_t ws_bytes, void* stream) {
+    if (x_dtype != BD_BF16) return BD_ERR_DTYPE;
+    return base_gemm_mx4(x, nullptr, false, T, d_in, n_mats, w_codes, w_scales, d_outs, ys,
+                         workspace, ws_bytes, stream);
+}
+
+size_t bd_base_gemm_mx4x4_n_workspace_bytes(int64_t T, int64_t d_in, int32_t n_mats,
+                                            const int64_t* d_outs) {
+    return mx4_n_workspace_bytes(true, T, d_in, n_mats, d_outs);
+}
+
+bd_status bd_base_gemm_mx4x4_n(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T,
+                               int64_t d_in, int32_t n_mats, const uint8_t* const* w_codes,
+                               const uint8_t* const* w_scales, const int64_t* d_outs,
+                               float* const* ys, void* workspace, size_t ws_bytes, void* stream) {
+    return base_gemm_mx4(x_codes, x_scales, true, T, d_in, n_mats, w_codes, w_scales, d_outs, ys,
+                         workspace, ws_bytes, stream);
+}
+
+// The workspace of bd_apply_mx4: the apply plan's | the quantised tokens | the base
+// product's.
+struct Mx4ApplyPlan {
+    ApplyPlan a;
+    bool x4 = false;
+    size_t off_xc = 0, off_xs = 0, off_base = 0, total = 0;
+};
+static bd_status make_mx4_plan(const bd_compress_params* p, int64_t T, int32_t n_users,
+                               int64_t d_out, int64_t d_in, bd_dtype x_dtype, bd_dtype y_dtype,
+                               bd_mx4_tokens tokens, Mx4ApplyPlan* pl) {
+    if (!p || (tokens != BD_MX4_TOKENS_BF16 && tokens != BD_MX4_TOKENS_MX4)) return BD_ERR_INVALID_ARG;
+    bd_status st = make_apply_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, &pl->a, false);
+    if (st != BD_OK) return st;
+    pl->x4 = tokens == BD_MX4_TOKENS_MX4;
+    if (x_dtype != BD_BF16 || !mx4_product_supported(pl->x4, T, d_in, d_out)) return BD_ERR_UNSUPPORTED;
+    size_t off = align_up(pl->a.total);
+    pl->off_xc = off;
+    if (pl->x4) off += align_up((size_t)T * d_in / 2);
+    pl->off_xs = off;
+    if (pl->x4) off += align_up((size_t)T * mx4_scale_stride(d_in));
+    pl->off_base = off;
+    if (T > 0) off += mx4_product_bytes(pl->x4, T, d_in, &d_out, 1);
+    pl->total = off;
+    return BD_OK;
+}
+
+size_t bd_apply_mx4_workspace_bytes(const bd_compress_params* p, int64_t T, int32_t n_users,
+                                    int64_t d_out, int64_t d_in, bd_dtype x_dtype,
+                                    bd_dtype y_dtype, bd_mx4_tokens tokens) {
+    Mx4ApplyPlan pl;
+    if (make_mx4_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, tokens, &pl) != BD_OK) return 0;
+    return pl.total;
+}
+
+bd_status bd_apply_mx4(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
+                       const uint8_t* w_codes, const uint8_t* w_scales, int64_t d_out,
+                       const uint64_t* signs_bank, const void* scales_bank,
+                       const bd_compress_params* p, int32_t n_users, const int32_t* user_ids,
+                       void* y, bd_dtype y_dtype, bd_mx4_tokens tokens, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    Mx4ApplyPlan pl;
+    bd_status st = make_mx4_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, tokens, &pl);
+    if (st != BD_OK) return st;
+    if (!workspace || ws_bytes < pl.total || !aligned(workspace, kAlign)) return BD_ERR_WORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    hipError_t e;
+    if (T > 0) {
+        if (!x || !w_codes || !w_scales || !y || !user_ids) return BD_ERR_INVALID_ARG;
+        if (n_users > 0 && (!signs_bank || !scales_bank)) return BD_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(y, 16) ||
+            !aligned(user_ids, 4) || (signs_bank && !aligned(signs_bank, 16)) ||
+            (scales_bank && !aligned(scales_bank, 16)))
+            return BD_ERR_INVALID_ARG;
+    }
+    e = launch_batch_prepare(pl.a.batch, x, user_ids, ws, s);
+    if (e != hipSuccess || T == 0) return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+    float* yacc = y_dtype == BD_F32 ? (float*)y : (float*)(ws + pl.a.off_yf);
+    const GemmMatArg m = {w_codes, yacc, d_out};
+    uint8_t *xc = (uint8_t*)(ws + pl.off_xc), *xs = (uint8_t*)(ws + pl.off_xs);
+    if (pl.x4) e = launch_mx4_quantize(x, BD_BF16, T, d_in, xc, xs, nullptr, s);
+    if (e == hipSuccess)
+        e = launch_mx4_product(pl.x4 ? (const void*)xc : x, pl.x4 ? xs : nullptr, T, d_in, &m,
+                               &w_scales, 1, pl.total > pl.off_base ? ws + pl.off_base : nullptr, s);
+    if (e == hipSuccess)
+        e = launch_delta(pl.a.batch, pl.a.delta, ws, x, signs_bank, scales_bank, yacc, s);
     if (e == hipSuccess && y_dtype == BD_BF16)
         e = launch_cast_bf16(yacc, (uint16_t*)y, T * d_out, s);
     return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;

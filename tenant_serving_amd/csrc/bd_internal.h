@@ -213,6 +213,22 @@ bool gemm_q8_supported(int64_t T, int64_t d_in, int64_t d_out);
 hipError_t launch_gemm_q8(const void* x, int64_t T, int64_t d_in, const int8_t* wq,
                           const float* wscale, int64_t d_out, float* y, hipStream_t s);
 
+// MX4 base weights and tokens (bd_mx4.hip): quantisation and the base products of up to
+// kMaxMats matrices that read the same tokens.  GemmMatArg::w holds a matrix's codes,
+// wscales its scale bytes; xscales: the tokens' scale bytes (x then holds MX4 codes), or
+// null for bf16 tokens.  mx4_product_bytes: the workspace the product uses (0: none);
+// without it (ws null) the launch needs none.
+inline int64_t mx4_scale_stride(int64_t cols) { return 16 * ((cols + 511) / 512); }
+hipError_t launch_mx4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                               uint8_t* scales, void* values, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                 int64_t cols, void* out, int odtype, hipStream_t s);
+bool mx4_product_supported(bool x4, int64_t T, int64_t d_in, int64_t d_out);
+size_t mx4_product_bytes(bool x4, int64_t T, int64_t d_in, const int64_t* d_outs, int n);
+hipError_t launch_mx4_product(const void* x, const uint8_t* xscales, int64_t T, int64_t d_in,
+                              const GemmMatArg* mats, const uint8_t* const* wscales, int n, char* ws,
+                              hipStream_t s);
+
 bool decode_path_supported(int xdtype, int64_t T, int mode);
 void make_decode_plan(int64_t T, int64_t d_in, DecodePlan* plan);
 hipError_t launch_decode_prep(const DecodePlan& pl, int U, const DeltaPlan& dp, const void* x,
