@@ -642,90 +642,121 @@ def bd_mx4_scale_stride(cols: int) -> int:
     return int(lib().bd_mx4_scale_stride(int(cols)))
 
 
-def _on(t: torch.Tensor):
-    """The tensor's device as the current one for the launches of a call."""
-    return torch.cuda.device(t.device)
+# A decode step is a chain of launches of a few microseconds, so these calls check their
+# tensors in one expression and leave the naming of what is wrong to _dev.
+
+def _need(t, name, dtype, shape, idx):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == idx and idx >= 0
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        _dev(t, name, (dtype,), shape, torch.device("cuda", idx) if idx >= 0 else None)
 
 
-def _mx4(codes, scales, name: str, device=None, cols: Optional[int] = None):
-    """(rows, cols) of an MX4 matrix after the checks of its two tensors."""
+def _run(f, idx, stream, *args) -> int:
+    """f(*args, stream) with device idx current (the launches need it)."""
+    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(None, stream)
+    if torch._C._cuda_getDevice() == idx:
+        return f(*args, raw)
+    with torch.cuda.device(idx):
+        return f(*args, raw)
+
+
+def _tokens_2d(x, name, dtypes):
+    """(device index, rows, columns) of a two-dimensional tensor of one of dtypes."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or x.dtype not in dtypes:
+        _dev(x, name, dtypes)
+        raise ValueError(f"{name} must be two-dimensional")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return x.get_device(), *x.shape
+
+
+def _mx4(codes, scales, name: str, idx=None, cols: Optional[int] = None):
+    """(device index, rows, cols) of an MX4 matrix after the checks of its two tensors."""
     if isinstance(codes, torch.Tensor) and (
             codes.dim() != 2 or (cols is not None and 2 * codes.shape[1] != cols)):
         raise ValueError(f"{name} codes have shape {tuple(codes.shape)}, expected (rows, "
                          f"{'cols' if cols is None else cols} / 2)")
-    _dev(codes, name + " codes", (torch.uint8,), None, device)
+    if idx is None:
+        _dev(codes, name + " codes", (torch.uint8,))
+        idx = codes.get_device()
+    _need(codes, name + " codes", torch.uint8, None, idx)
     rows, cols = codes.shape[0], 2 * codes.shape[1]
-    _dev(scales, name + " scales", (torch.uint8,), (rows, 16 * ((cols + 511) // 512)),
-         codes.device)
-    return rows, cols
+    _need(scales, name + " scales", torch.uint8, (rows, 16 * ((cols + 511) // 512)), idx)
+    return idx, rows, cols
 
 
 def bd_quantize_mx4(w, codes_out, scales_out, values_out=None, stream=None) -> int:
-    _dev(w, "w", (torch.float32, torch.bfloat16))
-    if w.dim() != 2:
-        raise ValueError("w must be two-dimensional")
-    rows, cols = w.shape
-    _dev(codes_out, "codes_out", (torch.uint8,), (rows, cols // 2), w.device)
-    _dev(scales_out, "scales_out", (torch.uint8,), (rows, 16 * ((cols + 511) // 512)), w.device)
-    _dev(values_out, "values_out", (w.dtype,), (rows, cols), w.device, optional=True)
-    with _on(w):
-        return int(lib().bd_quantize_mx4(_ptr(w), _dtype_code(w), rows, cols, _ptr(codes_out),
-                                         _ptr(scales_out), _ptr(values_out), _stream(w, stream)))
+    idx, rows, cols = _tokens_2d(w, "w", (torch.float32, torch.bfloat16))
+    _need(codes_out, "codes_out", torch.uint8, (rows, cols // 2), idx)
+    _need(scales_out, "scales_out", torch.uint8, (rows, 16 * ((cols + 511) // 512)), idx)
+    if values_out is not None:
+        _need(values_out, "values_out", w.dtype, (rows, cols), idx)
+    return _quantize_mx4(w, idx, rows, cols, codes_out, scales_out, values_out, stream)
+
+
+def _quantize_mx4(w, idx, rows, cols, codes, scales, values, stream) -> int:
+    return _run(lib().bd_quantize_mx4, idx, stream, w.data_ptr(), _dtype_code(w), rows, cols,
+                codes.data_ptr(), scales.data_ptr(), None if values is None else values.data_ptr())
 
 
 def bd_dequantize_mx4(codes, scales, out, stream=None) -> int:
-    rows, cols = _mx4(codes, scales, "base")
+    idx, rows, cols = _mx4(codes, scales, "base")
     _dev(out, "out", (torch.float32, torch.bfloat16), (rows, cols), codes.device)
-    with _on(out):
-        return int(lib().bd_dequantize_mx4(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
-                                           _dtype_code(out), _stream(out, stream)))
+    return _run(lib().bd_dequantize_mx4, idx, stream, codes.data_ptr(), scales.data_ptr(), rows,
+                cols, out.data_ptr(), _dtype_code(out))
 
 
-def _mx4_mats(T, d_in, bases, ys, workspace, device):
-    if not 1 <= len(bases) <= 4 or len(ys) != len(bases):
+def _mx4_bases(bases, idx, d_in):
+    """Row counts of 1..4 MX4 matrices on device idx, after their checks."""
+    if not 1 <= len(bases) <= 4:
+        raise ValueError("1..4 matrices")
+    return [_mx4(codes, scales, "base", idx, d_in)[1] for codes, scales in bases]
+
+
+def _mx4_outs(ys, T, rows, workspace, idx):
+    if len(ys) != len(rows):
         raise ValueError("1..4 matrices, one output each")
-    for (codes, scales), y in zip(bases, ys):
-        rows, _ = _mx4(codes, scales, "base", device, d_in)
-        _dev(y, "y", (torch.float32,), (T, rows), device)
-    _dev(workspace, "workspace", None, None, device, optional=True)
-    return (len(ys), _ptr_array([c for c, _ in bases]), _ptr_array([s for _, s in bases]),
-            (ctypes.c_int64 * len(ys))(*[c.shape[0] for c, _ in bases]), _ptr_array(ys),
-            _ptr(workspace), 0 if workspace is None else _nbytes(workspace))
+    for y, n in zip(ys, rows):
+        _need(y, "y", torch.float32, (T, n), idx)
+    if workspace is not None:
+        _dev(workspace, "workspace", None, None, ys[0].device)
+
+
+def _mx4_args(bases, rows, ys, ws):
+    n = len(rows)
+    P, N = ctypes.c_void_p * n, ctypes.c_int64 * n
+    return (n, P(*[c.data_ptr() for c, _ in bases]), P(*[s.data_ptr() for _, s in bases]), N(*rows),
+            P(*[y.data_ptr() for y in ys]), None if ws is None else ws.data_ptr(),
+            0 if ws is None else _nbytes(ws))
 
 
 def bd_base_gemm_mx4_n_workspace_bytes(T: int, d_in: int, d_outs) -> int:
     arr = (ctypes.c_int64 * len(d_outs))(*[int(d) for d in d_outs])
-    return int(lib().bd_base_gemm_mx4_n_workspace_bytes(T, d_in, len(d_outs), arr))
+    return lib().bd_base_gemm_mx4_n_workspace_bytes(T, d_in, len(d_outs), arr)
 
 
 def bd_base_gemm_mx4_n(x, bases, ys, workspace=None, stream=None) -> int:
     """Base products of bf16 tokens with up to 4 MX4 matrices; bases: (codes, scales) of
     each, ys: fp32 outputs, `workspace` sized by the query (None: no split of K)."""
-    _dev(x, "x", (torch.bfloat16,))
-    T, d_in = x.shape
-    args = _mx4_mats(T, d_in, bases, ys, workspace, x.device)
-    with _on(x):
-        return int(lib().bd_base_gemm_mx4_n(_ptr(x), BD_BF16, T, d_in, *args, _stream(x, stream)))
+    idx, T, d_in = _tokens_2d(x, "x", (torch.bfloat16,))
+    rows = _mx4_bases(bases, idx, d_in)
+    _mx4_outs(ys, T, rows, workspace, idx)
+    return _run(lib().bd_base_gemm_mx4_n, idx, stream, x.data_ptr(), BD_BF16, T, d_in,
+                *_mx4_args(bases, rows, ys, workspace))
 
 
 def bd_base_gemm_mx4x4_n_workspace_bytes(T: int, d_in: int, d_outs) -> int:
     arr = (ctypes.c_int64 * len(d_outs))(*[int(d) for d in d_outs])
-    return int(lib().bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, len(d_outs), arr))
+    return lib().bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, len(d_outs), arr)
 
 
 def bd_base_gemm_mx4x4_n(x_codes, x_scales, bases, ys, workspace=None, stream=None) -> int:
     """bd_base_gemm_mx4_n on MX4 tokens (codes and scales of bd_quantize_mx4)."""
-    T, d_in = _mx4(x_codes, x_scales, "token")
-    args = _mx4_mats(T, d_in, bases, ys, workspace, x_codes.device)
-    with _on(x_codes):
-        return int(lib().bd_base_gemm_mx4x4_n(_ptr(x_codes), _ptr(x_scales), T, d_in, *args,
-                                              _stream(x_codes, stream)))
-
-
-def bd_apply_mx4_workspace_bytes(p, T: int, n_users: int, d_out: int, d_in: int, x_dtype: int,
-                                 y_dtype: int, tokens="bf16") -> int:
-    return int(lib().bd_apply_mx4_workspace_bytes(ctypes.byref(p), T, n_users, d_out, d_in,
-                                                  x_dtype, y_dtype, _tokens(tokens)))
+    idx, T, d_in = _mx4(x_codes, x_scales, "token")
+    rows = _mx4_bases(bases, idx, d_in)
+    _mx4_outs(ys, T, rows, workspace, idx)
+    return _run(lib().bd_base_gemm_mx4x4_n, idx, stream, x_codes.data_ptr(), x_scales.data_ptr(), T,
+                d_in, *_mx4_args(bases, rows, ys, workspace))
 
 
 def _tokens(tokens) -> int:
@@ -736,32 +767,48 @@ def _tokens(tokens) -> int:
     return int(tokens)
 
 
+def bd_apply_mx4_workspace_bytes(p, T: int, n_users: int, d_out: int, d_in: int, x_dtype: int,
+                                 y_dtype: int, tokens="bf16") -> int:
+    return lib().bd_apply_mx4_workspace_bytes(ctypes.byref(p), T, n_users, d_out, d_in, x_dtype,
+                                              y_dtype, _tokens(tokens))
+
+
+def _apply_mx4_checks(x, codes, scales, signs_bank, scales_bank, p, n_users, user_ids):
+    idx, T, d_in = _tokens_2d(x, "x", (torch.bfloat16, torch.float32))
+    _, d_out, _ = _mx4(codes, scales, "base", idx, d_in)
+    _need(signs_bank, "signs_bank", torch.int64, (n_users, d_out, d_in // 64), idx)
+    _scales(scales_bank, p, n_users, d_out, d_in, x.device)
+    _need(user_ids, "user_ids", torch.int32, (T,), idx)
+    return idx, T, d_in, d_out
+
+
+def _apply_mx4(x, idx, T, d_in, d_out, codes, scales, signs_bank, scales_bank, p, n_users,
+               user_ids, y, ws, tokens, stream) -> int:
+    return _run(lib().bd_apply_mx4, idx, stream, x.data_ptr(), _dtype_code(x), T, d_in,
+                codes.data_ptr(), scales.data_ptr(), d_out, signs_bank.data_ptr(),
+                scales_bank.data_ptr(), ctypes.byref(p), int(n_users), user_ids.data_ptr(),
+                y.data_ptr(), _dtype_code(y), tokens, ws.data_ptr(), _nbytes(ws))
+
+
 def bd_apply_mx4(x, codes, scales, signs_bank, scales_bank, p, n_users, user_ids, y, workspace,
                  tokens="bf16", stream=None) -> int:
-    _dev(x, "x", (torch.float32, torch.bfloat16))
-    T, d_in = x.shape
-    dev = x.device
-    d_out, _ = _mx4(codes, scales, "base", dev, d_in)
-    _bank(signs_bank, scales_bank, p, n_users, d_out, d_in, dev)
-    _ids(user_ids, T, dev)
-    _dev(y, "y", (torch.float32, torch.bfloat16), (T, d_out), dev)
-    _dev(workspace, "workspace", None, None, dev)
-    with _on(x):
-        return int(lib().bd_apply_mx4(_ptr(x), _dtype_code(x), T, d_in, _ptr(codes), _ptr(scales),
-                                      d_out, _ptr(signs_bank), _ptr(scales_bank), ctypes.byref(p),
-                                      int(n_users), _ptr(user_ids), _ptr(y), _dtype_code(y),
-                                      _tokens(tokens), _ptr(workspace), _nbytes(workspace),
-                                      _stream(x, stream)))
+    """bd_apply on an MX4 base; tokens: "bf16" or "mx4", how the base product takes x."""
+    idx, T, d_in, d_out = _apply_mx4_checks(x, codes, scales, signs_bank, scales_bank, p, n_users,
+                                            user_ids)
+    _dev(y, "y", (torch.float32, torch.bfloat16), (T, d_out), x.device)
+    _dev(workspace, "workspace", None, None, x.device)
+    return _apply_mx4(x, idx, T, d_in, d_out, codes, scales, signs_bank, scales_bank, p, n_users,
+                      user_ids, y, workspace, _tokens(tokens), stream)
 
 
 def quantize_mx4(w: torch.Tensor, values: bool = False, stream=None):
     """(codes, scales) of w in MX4, and with `values` also what they stand for, in w's
     dtype (bd_quantize_mx4)."""
-    rows, cols = w.shape
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((rows, 16 * ((cols + 511) // 512)), dtype=torch.uint8, device=w.device)
+    idx, rows, cols = _tokens_2d(w, "w", (torch.float32, torch.bfloat16))
+    codes = w.new_empty((rows, cols // 2), dtype=torch.uint8)
+    scales = w.new_empty((rows, 16 * ((cols + 511) // 512)), dtype=torch.uint8)
     out = torch.empty_like(w) if values else None
-    _check(bd_quantize_mx4(w, codes, scales, out, stream), "bd_quantize_mx4")
+    _check(_quantize_mx4(w, idx, rows, cols, codes, scales, out, stream), "bd_quantize_mx4")
     return (codes, scales, out) if values else (codes, scales)
 
 
@@ -774,26 +821,32 @@ def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bf
 
 def base_gemm_mx4(x: torch.Tensor, bases, ws=None, stream=None):
     """[x . W^T] in fp32 for 1..4 MX4 matrices (codes, scales) and bf16 tokens x."""
-    T, d_in = x.shape
-    outs = [c.shape[0] for c, _ in bases]
-    ys = [torch.empty((T, n), dtype=torch.float32, device=x.device) for n in outs]
+    idx, T, d_in = _tokens_2d(x, "x", (torch.bfloat16,))
+    rows = _mx4_bases(bases, idx, d_in)
+    ys = [x.new_empty((T, n), dtype=torch.float32) for n in rows]
     if ws is None:
-        need = bd_base_gemm_mx4_n_workspace_bytes(T, d_in, outs)
+        need = bd_base_gemm_mx4_n_workspace_bytes(T, d_in, rows)
         ws = workspace(need, x.device) if need > 0 else None
-    _check(bd_base_gemm_mx4_n(x, bases, ys, ws, stream), "bd_base_gemm_mx4_n")
+    else:
+        _dev(ws, "workspace", None, None, x.device)
+    _check(_run(lib().bd_base_gemm_mx4_n, idx, stream, x.data_ptr(), BD_BF16, T, d_in,
+                *_mx4_args(bases, rows, ys, ws)), "bd_base_gemm_mx4_n")
     return ys
 
 
 def base_gemm_mx4x4(xq, bases, ws=None, stream=None):
     """base_gemm_mx4 on MX4 tokens xq = (codes, scales)."""
     x_codes, x_scales = xq
-    T, d_in = x_codes.shape[0], 2 * x_codes.shape[1]
-    outs = [c.shape[0] for c, _ in bases]
-    ys = [torch.empty((T, n), dtype=torch.float32, device=x_codes.device) for n in outs]
+    idx, T, d_in = _mx4(x_codes, x_scales, "token")
+    rows = _mx4_bases(bases, idx, d_in)
+    ys = [x_codes.new_empty((T, n), dtype=torch.float32) for n in rows]
     if ws is None:
-        need = bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, outs)
+        need = bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, rows)
         ws = workspace(need, x_codes.device) if need > 0 else None
-    _check(bd_base_gemm_mx4x4_n(x_codes, x_scales, bases, ys, ws, stream), "bd_base_gemm_mx4x4_n")
+    else:
+        _dev(ws, "workspace", None, None, x_codes.device)
+    _check(_run(lib().bd_base_gemm_mx4x4_n, idx, stream, x_codes.data_ptr(), x_scales.data_ptr(), T,
+                d_in, *_mx4_args(bases, rows, ys, ws)), "bd_base_gemm_mx4x4_n")
     return ys
 
 
@@ -801,14 +854,16 @@ def apply_mx4(x, codes, scales, signs_bank, scales_bank, p, user_ids, y_dtype=to
               tokens="bf16", ws=None, stream=None, check: bool = False) -> torch.Tensor:
     """bd_apply on an MX4 base (codes, scales); tokens: how the base product reads x,
     "bf16" as it is or "mx4" quantised within the call."""
-    T, d_in = x.shape
-    d_out, U = codes.shape[0], signs_bank.shape[0]
-    y = torch.empty((T, d_out), dtype=y_dtype, device=x.device)
+    U, tok = signs_bank.shape[0], _tokens(tokens)
+    idx, T, d_in, d_out = _apply_mx4_checks(x, codes, scales, signs_bank, scales_bank, p, U, user_ids)
+    y = x.new_empty((T, d_out), dtype=y_dtype)
     if ws is None:
         ws = workspace(bd_apply_mx4_workspace_bytes(p, T, U, d_out, d_in, _dtype_code(x),
-                                                    _dtype_code(y), tokens), x.device)
-    _check(bd_apply_mx4(x, codes, scales, signs_bank, scales_bank, p, U, user_ids, y, ws, tokens,
-                        stream), "bd_apply_mx4")
+                                                    _dtype_code(y), tok), x.device)
+    else:
+        _dev(ws, "workspace", None, None, x.device)
+    _check(_apply_mx4(x, idx, T, d_in, d_out, codes, scales, signs_bank, scales_bank, p, U, user_ids,
+                      y, ws, tok, stream), "bd_apply_mx4")
     if check:
         _check(bd_device_status(ws, stream), "bd_apply_mx4 (device)")
     return y

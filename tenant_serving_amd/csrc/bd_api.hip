@@ -541,18 +541,21 @@ bd_status bd_base_gemm_mx4x4_n(const uint8_t* x_codes, const uint8_t* x_scales, 
 // product's.
 struct Mx4ApplyPlan {
     ApplyPlan a;
-    bool x4 = false;
+    bool x4 = false, dec = false;  // dec: the one-launch decode path
     size_t off_xc = 0, off_xs = 0, off_base = 0, total = 0;
 };
 static bd_status make_mx4_plan(const bd_compress_params* p, int64_t T, int32_t n_users,
                                int64_t d_out, int64_t d_in, bd_dtype x_dtype, bd_dtype y_dtype,
                                bd_mx4_tokens tokens, Mx4ApplyPlan* pl) {
     if (!p || (tokens != BD_MX4_TOKENS_BF16 && tokens != BD_MX4_TOKENS_MX4)) return BD_ERR_INVALID_ARG;
-    bd_status st = make_apply_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, &pl->a, false);
-    if (st != BD_OK) return st;
     pl->x4 = tokens == BD_MX4_TOKENS_MX4;
+    pl->dec = !pl->x4 && q8_path_supported(x_dtype, T, p->mode, d_in);
+    bd_status st = make_apply_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, &pl->a, pl->dec);
+    if (st != BD_OK) return st;
     if (x_dtype != BD_BF16 || !mx4_product_supported(pl->x4, T, d_in, d_out)) return BD_ERR_UNSUPPORTED;
     size_t off = align_up(pl->a.total);
+    pl->total = off;
+    if (pl->dec) return BD_OK;
     pl->off_xc = off;
     if (pl->x4) off += align_up((size_t)T * d_in / 2);
     pl->off_xs = off;
@@ -591,6 +594,11 @@ bd_status bd_apply_mx4(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
             !aligned(user_ids, 4) || (signs_bank && !aligned(signs_bank, 16)) ||
             (scales_bank && !aligned(scales_bank, 16)))
             return BD_ERR_INVALID_ARG;
+    }
+    if (pl.dec) {
+        e = launch_decode_mx4(T, n_users, d_in, pl.a.delta, x, user_ids, w_codes, w_scales,
+                              signs_bank, scales_bank, y, y_dtype, ws, s);
+        return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
     }
     e = launch_batch_prepare(pl.a.batch, x, user_ids, ws, s);
     if (e != hipSuccess || T == 0) return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;

@@ -912,14 +912,20 @@ constexpr int kUnitRing = 8;
 // half the base bytes.  A ring item then carries 16 columns per lane, two MFMA steps,
 // whose codes are widened to bf16 exactly (|q| <= 127 has 7 significant bits); the
 // base sum is multiplied by the row's scale in the epilogue.
-template <int MODE, bool Q8>
+// MX4: the base weight as MX4 rows (bd_mx4.hip; wscale: their scale bytes), a quarter of
+// the base bytes: a ring item carries one 32-column block per lane, four MFMA steps, whose
+// codes are widened to bf16 with their scale (exact); the 16 scale bytes of a row's unit
+// are loaded once.
+enum { kBaseBf16 = 0, kBaseInt8 = 1, kBaseMx4 = 2 };
+template <int MODE, int FMT>
 __global__ void __launch_bounds__(64 * kUnitWaves)
 k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, int T, int U,
-              int64_t d_in, const void* __restrict__ w, const float* __restrict__ wscale,
+              int64_t d_in, const void* __restrict__ w, const void* __restrict__ wscale,
               int64_t d_out, const uint64_t* __restrict__ signs, uint64_t sstride,
               const void* __restrict__ scales, int sdtype, int64_t per_user, void* __restrict__ y,
               int ydtype,
               uint32_t* __restrict__ status) {
+    constexpr bool Q8 = FMT == kBaseInt8, MX4 = FMT == kBaseMx4;
     __shared__ f32x4 red[2 * kUnitWaves * 64];  // base then delta partial tiles, wave order
     __shared__ __attribute__((aligned(16))) char xlds[kUnitWaves * 16384];
     const int lane = threadIdx.x & 63;
@@ -982,17 +988,19 @@ k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, i
     const int nsegR = (nseg + kUnitRing - 1) / kUnitRing * kUnitRing;
     const int64_t bank_row = d_in / 8;
     const uint64_t user_bytes = (uint64_t)d_out * (uint64_t)bank_row;
-    constexpr int kWBytes = Q8 ? 1 : 2;  // bytes per base weight
-    constexpr int kWItems = Q8 ? 8 : 16;  // base ring items per unit
-    const uint64_t w_bytes = (uint64_t)d_out * (uint64_t)d_in * kWBytes;
+    constexpr int kWHalf = MX4 ? 1 : Q8 ? 2 : 4;            // half bytes per base weight
+    constexpr int kWItems = MX4 ? 4 : Q8 ? 8 : 16;          // base ring items per unit
+    constexpr int kWCols = MX4 ? 32 : Q8 ? 16 : 8;          // columns of a lane's item
+    const uint64_t w_bytes = (uint64_t)d_out * (uint64_t)d_in * kWHalf / 2;
     // lane (m, g): sign bytes of row rowA for columns 512 w + 128 g .. + 127 (word q: k-group
     // g of product q); W_base columns 512 w + 32 s + 8 g .. + 7 of row rowA (Q8: the INT8
-    // codes of columns 512 w + 64 s + 16 g .. + 15, steps 2 s and 2 s + 1)
+    // codes of columns 512 w + 64 s + 16 g .. + 15, steps 2 s and 2 s + 1; MX4: those of block
+    // 16 w + 4 s + g)
     const uint32_t soff = (int64_t)512 * wv + 128 * g < d_in
                               ? (uint32_t)(rowA * bank_row + 64 * wv + 16 * g)
                               : kOOB;
-    const int64_t c0 = (int64_t)512 * wv + (Q8 ? 16 : 8) * g;
-    const uint32_t woff = (uint32_t)((rowA * d_in + c0) * kWBytes);
+    const int64_t c0 = (int64_t)512 * wv + kWCols * g;
+    const uint32_t woff = (uint32_t)((rowA * d_in + c0) * kWHalf / 2);
     // (branch-free: a branch here splits the loop body into blocks, and the compiler then
     // gathers the products of a whole iteration at its end)
     const uint64_t wbase = (uint64_t)(uintptr_t)w;
@@ -1004,11 +1012,18 @@ k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, i
         const uint64_t base = wbase + ((sbase - wbase) & msk);
         const uint64_t bytes = w_bytes + ((user_bytes - w_bytes) & msk);
         const uint32_t so = i < nseg ? soff : kOOB;
-        const bool okw = ((uint32_t)s < (uint32_t)kWItems) & (c0 + (Q8 ? 64 : 32) * s < d_in);
+        const bool okw = ((uint32_t)s < (uint32_t)kWItems) & (c0 + 4 * kWCols * s < d_in);
         const uint32_t wo = okw ? woff + 64u * (uint32_t)s : kOOB;  // no short-circuit branch
         const uint32_t off = wo + ((so - wo) & (uint32_t)msk);
         return buf_load16(make_rsrc((const void*)(uintptr_t)base, bytes), off);
     };
+    u32x4 wexp = {0u, 0u, 0u, 0u};  // MX4: the scale bytes of row rowA's unit
+    if (MX4) {
+        const uint64_t ld = 16u * (uint64_t)((d_in + 511) / 512);
+        wexp = buf_load16(make_rsrc(wscale, (uint64_t)d_out * ld),
+                          (int64_t)512 * wv < d_in ? (uint32_t)(rowA * (int64_t)ld + 16 * wv) : kOOB);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     u32x4 ring[kUnitRing];
 #pragma unroll
     for (int r = 0; r < kUnitRing; ++r) {
@@ -1022,7 +1037,7 @@ k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, i
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t o = r0 + 4 * g + e;
-            wsc[e] = wscale[o < d_out ? o : d_out - 1];
+            wsc[e] = ((const float*)wscale)[o < d_out ? o : d_out - 1];
         }
     }
     if (wv == 0 && tok_user >= 0 && m < T) {
@@ -1146,6 +1161,22 @@ k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, i
             const u32x4 a0 = {v[0], v[1], v[2], v[3]}, a1 = {v[4], v[5], v[6], v[7]};
             accb = mfma_bf16(a0, b0, accb);
             accb = mfma_bf16(a1, b1, accb);
+            ring[s % kUnitRing] = load_item(nsegR + s + kUnitRing);  // empty past the unit
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (MX4) {
+        // item s: lane (m, g) holds the codes of columns 128 s + 32 g .. + 31 of row m; the
+        // tokens of columns 8 j .. 8 j + 7 of that block are LDS chunk 16 s + 4 g + j
+#pragma unroll
+        for (int s = 0; s < kWItems; ++s) {
+            const u32x4 c = ring[s % kUnitRing];
+            const uint32_t es = s == 0 ? wexp.x : s == 1 ? wexp.y : s == 2 ? wexp.z : wexp.w;
+            const float f = __uint_as_float(((es >> (8 * g)) & 255u) << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const u32x4 b = *(const u32x4*)(xs + xslot(m, 16 * s + 4 * g + j, 1024u));
+                accb = mfma_bf16(widen_mx4(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w, f), b, accb);
+            }
             ring[s % kUnitRing] = load_item(nsegR + s + kUnitRing);  // empty past the unit
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -1285,13 +1316,29 @@ hipError_t launch_decode_q8(int64_t T, int U, int64_t d_in, const DeltaPlan& dp,
                             hipStream_t s) {
     const dim3 grid((unsigned)((dp.d_out + 15) / 16));
 #define BD_UNITQ(MODE)                                                                        \
-    k_decode_unit<MODE, true><<<grid, dim3(64 * kUnitWaves), 0, s>>>(                         \
+    k_decode_unit<MODE, kBaseInt8><<<grid, dim3(64 * kUnitWaves), 0, s>>>(                         \
         (const uint16_t*)x, ids, (int)T, U, d_in, wq, wscale, dp.d_out, signs,                   \
         sign_stride(dp.sstride, dp.d_out, d_in), scales, dp.sdtype, scale_stride(dp), y, ydtype,  \
         (uint32_t*)ws)
     if (dp.mode == BD_SCALE_MATRIX) BD_UNITQ(BD_SCALE_MATRIX);
     else BD_UNITQ(BD_SCALE_ROW);
 #undef BD_UNITQ
+    return hipGetLastError();
+}
+
+hipError_t launch_decode_mx4(int64_t T, int U, int64_t d_in, const DeltaPlan& dp, const void* x,
+                             const int32_t* ids, const uint8_t* codes, const uint8_t* wscales,
+                             const uint64_t* signs, const void* scales, void* y, int ydtype, char* ws,
+                             hipStream_t s) {
+    const dim3 grid((unsigned)((dp.d_out + 15) / 16));
+#define BD_UNITX(MODE)                                                                        \
+    k_decode_unit<MODE, kBaseMx4><<<grid, dim3(64 * kUnitWaves), 0, s>>>(                     \
+        (const uint16_t*)x, ids, (int)T, U, d_in, codes, wscales, dp.d_out, signs,               \
+        sign_stride(dp.sstride, dp.d_out, d_in), scales, dp.sdtype, scale_stride(dp), y, ydtype,  \
+        (uint32_t*)ws)
+    if (dp.mode == BD_SCALE_MATRIX) BD_UNITX(BD_SCALE_MATRIX);
+    else BD_UNITX(BD_SCALE_ROW);
+#undef BD_UNITX
     return hipGetLastError();
 }
 
@@ -1304,7 +1351,7 @@ hipError_t launch_decode_fused(int64_t T, int U, int64_t d_in, const DeltaPlan& 
     const dim3 grid((unsigned)((dp.d_out + 15) / 16));
     if (dpad <= 512 * kUnitWaves) {
 #define BD_UNIT(MODE)                                                                         \
-    k_decode_unit<MODE, false><<<grid, dim3(64 * kUnitWaves), 0, s>>>(                        \
+    k_decode_unit<MODE, kBaseBf16><<<grid, dim3(64 * kUnitWaves), 0, s>>>(                        \
         (const uint16_t*)x, ids, (int)T, U, d_in, wb, nullptr, dp.d_out, signs,                  \
         sign_stride(dp.sstride, dp.d_out, d_in), scales, dp.sdtype, scale_stride(dp), y, ydtype,  \
         (uint32_t*)ws)

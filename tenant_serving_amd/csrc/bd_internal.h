@@ -229,6 +229,12 @@ hipError_t launch_mx4_product(const void* x, const uint8_t* xscales, int64_t T, 
                               const GemmMatArg* mats, const uint8_t* const* wscales, int n, char* ws,
                               hipStream_t s);
 
+// The one-launch decode apply on MX4 rows, for the batches and rows of q8_path_supported.
+hipError_t launch_decode_mx4(int64_t T, int U, int64_t d_in, const DeltaPlan& dp, const void* x,
+                             const int32_t* ids, const uint8_t* codes, const uint8_t* wscales,
+                             const uint64_t* signs, const void* scales, void* y, int ydtype, char* ws,
+                             hipStream_t s);
+
 bool decode_path_supported(int xdtype, int64_t T, int mode);
 void make_decode_plan(int64_t T, int64_t d_in, DecodePlan* plan);
 hipError_t launch_decode_prep(const DecodePlan& pl, int U, const DeltaPlan& dp, const void* x,
@@ -290,6 +296,18 @@ __device__ __forceinline__ float f16_to_f32(uint16_t h) {
     return (float)v;
 }
 
+
+// Eight MX4 codes (one dword, low nibble first) as four bf16 pairs, each code times the
+// scale: exact (2 significant bits), Inf where the product leaves the range of bf16.
+typedef unsigned int mx4_u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ mx4_u32x4 widen_mx4(uint32_t c, float scale) {
+    mx4_u32x4 v;
+    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
+    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
+    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
+    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+    return v;
+}
 
 // The fp6 e2m3 B operands of the block-scaled MFMA 16x16x128 for one lane's 32
 // values (one 32-column block of one token): R[p] holds the bf16 values of

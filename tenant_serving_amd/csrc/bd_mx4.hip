@@ -97,17 +97,6 @@ struct MatId {
     const MatId mt = {BD_PICK(gm, mt##_i, w),    BD_PICK(gm, mt##_i, s), BD_PICK(gm, mt##_i, y), \
                       BD_PICK(gm, mt##_i, part), BD_PICK(gm, mt##_i, N), BD_PICK(gm, mt##_i, rt_begin)}
 
-// Eight codes (one dword, low nibble first) as four bf16 pairs, each code times the
-// scale: exact (2 significant bits), Inf where the product leaves the range of bf16.
-__device__ __forceinline__ u32x4 widen_mx4(uint32_t c, float scale) {
-    u32x4 v;
-    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
-    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
-    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
-    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
-    return v;
-}
-
 // Eight consecutive columns of a row, as loaded.
 template <typename WT>
 struct Cols8;

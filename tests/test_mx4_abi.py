@@ -150,6 +150,6 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="contiguous"):
         B._dev(c.t(), "base codes", (u8,))
     with pytest.raises(ValueError, match="1..4 matrices"):
-        B._mx4_mats(4, 128, [], [], None, None)
+        B._mx4_bases([], 0, 128)
     with pytest.raises(ValueError, match="tokens is"):
         B._tokens("fp8")
