@@ -233,109 +233,87 @@ k_mx4_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ 
     }
 }
 
-// The product for batches of at most 16 tokens, where the codes' stream is all that
-// counts.  Wave w of a block holds the tokens of its own 512 columns (of the 4096 of K part
-// p) in registers as operands, loaded once; the block then walks over 16-row tiles, each
-// wave streaming 256 bytes of codes and 16 of scales per row, the next tile's loads in
-// flight behind the products, and the eight partial tiles are summed in LDS in wave order.
-// bf16 tokens: a lane's block of 32 columns, widened to bf16 (exact), feeds four
-// v_mfma_f32_16x16x32_bf16, step j taking columns 8 j .. 8 j + 7 of every block.  MX4
-// tokens: one block-scaled 16x16x128 product per 128 columns.
-// K parts: part blockIdx.y of gridDim.y writes its partial sums to part; with one grid row
-// a block takes all `parts` in turn and adds into y.
-constexpr int kRowsWaves = 8, kRowsK = 512 * kRowsWaves, kRowsMaxT = 16;
+// The product for batches of at most 16 tokens on matrices of few rows and at most 4096
+// columns, where a launch's latency is all that counts: one block per 16 rows, wave w on
+// columns 512 w .. 512 w + 511, every load issued at once, the eight partial tiles summed in
+// LDS in wave order.  bf16 tokens: a lane's block of 32 columns, widened to bf16 (exact),
+// feeds four v_mfma_f32_16x16x32_bf16, step j taking columns 8 j .. 8 j + 7 of every block.
+// MX4 tokens: one block-scaled 16x16x128 product per 128 columns.
+// Every block reads all tokens, so the tiles below win from some rows on.  Against them
+// (graph replays, us, 4096 columns): bf16, 6144 rows: 6.3 / 8.9 at 1 token, 8.9 / 9.3 at 8,
+// 10.2 / 9.4 at 12; 4096 rows: 7.0 / 8.9 at 16; 14336 rows: 11.1 / 10.6 at 1.  MX4, 6144 rows:
+// 5.7 / 7.5 at 1, 8.0 / 8.2 at 16; 14336 rows: 11.0 / 9.1 at 8.
+constexpr int kRowsWaves = 8, kRowsK = 512 * kRowsWaves;
+inline bool rows_fit(bool x4, int64_t T, int64_t d_in, int64_t row_tiles) {
+    return T <= 16 && d_in <= kRowsK && row_tiles * (x4 ? 12 : T + 8) <= 6144;
+}
 template <bool X4>
-__global__ void __launch_bounds__(64 * kRowsWaves, 4)
+__global__ void __launch_bounds__(64 * kRowsWaves)
 k_mx4_rows(const void* __restrict__ x, const uint8_t* __restrict__ xs, const GemmMats gm, int T,
-           int K, int parts) {
-    __shared__ f32x4 red[2][kRowsWaves][64];
+           int K) {
+    __shared__ f32x4 red[kRowsWaves][64];
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const int nrt = gm.rt_begin[gm.n];
     const uint32_t rowb = (uint32_t)(K / 2), ld = 16u * (uint32_t)((K + 511) / 512);
+    BD_MAT_OF(mt, gm, (int)blockIdx.x);
+    const int N = mt.N, r0 = 16 * ((int)blockIdx.x - mt.rt0);
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(mt.w, (uint64_t)N * rowb);
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(mt.s, (uint64_t)N * ld);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(x, X4 ? (uint64_t)T * rowb : (uint64_t)T * K * 2);
     const __amdgpu_buffer_rsrc_t er = make_rsrc(xs, X4 ? (uint64_t)T * ld : 0);
-    const int p0 = gridDim.y > 1 ? (int)blockIdx.y : 0, p1 = gridDim.y > 1 ? p0 + 1 : parts;
-    for (int p = p0; p < p1; ++p) {
-        const int b0 = (p * kRowsK + 512 * wv) / 32 + g;  // this lane's blocks: b0 + 4 s
-        // the tokens: lane (m, g) holds token m's blocks b0 + 4 s
-        u32x4 Xv[X4 ? 4 : 16];
-        uint32_t xe[4] = {0u, 0u, 0u, 0u};
+    const int b0 = 16 * wv + g;  // this lane's blocks of 32 columns: b0 + 4 s
+    const uint32_t row = (uint32_t)(r0 + m);
+    u32x4 C[4], Xv[X4 ? 4 : 16];
+    uint32_t xe[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const bool ok = m < T && b0 + 4 * s < K / 32;
-            if constexpr (X4) {
-                Xv[s] = buf_load16(xr, ok ? (uint32_t)m * rowb + 16u * (uint32_t)(b0 + 4 * s) : kOOB);
-                xe[s] = buf_load1(er, ok ? (uint32_t)m * ld + (uint32_t)(b0 + 4 * s) : kOOB);
-            } else {
+    for (int s = 0; s < 4; ++s)
+        C[s] = buf_load16(wr, r0 + m < N && b0 + 4 * s < K / 32 ? row * rowb + 16u * (uint32_t)(b0 + 4 * s) : kOOB);
+    // the 16 scale bytes of the row's 512 columns
+    const u32x4 E = buf_load16(sr, r0 + m < N && 512 * wv < K ? row * ld + 16u * (uint32_t)wv : kOOB);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    Xv[4 * s + j] = buf_load16(
-                        xr, ok ? (uint32_t)m * (uint32_t)(2 * K) + 64u * (uint32_t)(b0 + 4 * s) + 16u * j : kOOB);
-            }
+    for (int s = 0; s < 4; ++s) {  // token m's same blocks
+        const bool ok = m < T && b0 + 4 * s < K / 32;
+        if constexpr (X4) {
+            Xv[s] = buf_load16(xr, ok ? (uint32_t)m * rowb + 16u * (uint32_t)(b0 + 4 * s) : kOOB);
+            xe[s] = buf_load1(er, ok ? (uint32_t)m * ld + (uint32_t)(b0 + 4 * s) : kOOB);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                Xv[4 * s + j] = buf_load16(
+                    xr, ok ? (uint32_t)m * (uint32_t)(2 * K) + 64u * (uint32_t)(b0 + 4 * s) + 16u * j : kOOB);
         }
-        u32x4 C[4], E;  // the tile's codes, and the 16 scale bytes of row m's 512 columns
-        auto load = [&](int rt) {
-            BD_MAT_OF(mt, gm, rt);
-            const int N = mt.N, row = 16 * (rt - mt.rt0) + m;
-            const bool okr = rt < nrt && row < N;
-            const __amdgpu_buffer_rsrc_t wr = make_rsrc(mt.w, (uint64_t)N * rowb);
-            const __amdgpu_buffer_rsrc_t sr = make_rsrc(mt.s, (uint64_t)N * ld);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-                C[s] = buf_load16(wr, okr && b0 + 4 * s < K / 32
-                                          ? (uint32_t)row * rowb + 16u * (uint32_t)(b0 + 4 * s) : kOOB);
-            E = buf_load16(sr, okr && b0 - g < K / 32 ? (uint32_t)row * ld + (uint32_t)(b0 - g) : kOOB);
-        };
-        int rt = (int)blockIdx.x, buf = 0;
-        if (rt < nrt) load(rt);
-        for (; rt < nrt; rt += (int)gridDim.x, buf ^= 1) {
-            u32x4 c[4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) c[s] = C[s];
-            const u32x4 e = E;
-            load(rt + (int)gridDim.x);  // (empty past the last tile)
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t es = s == 0 ? e.x : s == 1 ? e.y : s == 2 ? e.z : e.w;
-                const uint32_t byte = (es >> (8 * g)) & 255u;
-                if constexpr (X4) {
-                    const i32x8 a8 = {(int)c[s].x, (int)c[s].y, (int)c[s].z, (int)c[s].w, 0, 0, 0, 0};
-                    const i32x8 b8 = {(int)Xv[s].x, (int)Xv[s].y, (int)Xv[s].z, (int)Xv[s].w, 0, 0, 0, 0};
-                    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, acc, 4, 4, 0, (int)byte, 0,
-                                                                           (int)xe[s]);
-                } else {
-                    const float f = mx4_scale(byte);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t d = j == 0 ? c[s].x : j == 1 ? c[s].y : j == 2 ? c[s].z : c[s].w;
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, widen_mx4(d, f)),
-                            __builtin_bit_cast(bf16x8, Xv[4 * s + j]), acc, 0, 0, 0);
-                    }
-                }
-            }
-            red[buf][wv][lane] = acc;
-            __syncthreads();  // (the other buffer's readers passed the tile before)
-            if (threadIdx.x < 256) {
-                const int t = threadIdx.x >> 4, r = threadIdx.x & 15;  // token, row
-                const int l = t + 16 * (r >> 2);  // D lane layout: column t, element r % 4
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < kRowsWaves; ++w) v += ((const float*)&red[buf][w][l])[r & 3];
-                BD_MAT_OF(mt, gm, rt);
-                const int N = mt.N, o = 16 * (rt - mt.rt0) + r;
-                if (t < T && o < N) {
-                    float* dst = gridDim.y > 1 ? mt.part + ((int64_t)p * T + t) * N + o
-                                               : mt.y + (int64_t)t * N + o;
-                    *dst = p > p0 ? *dst + v : v;
-                }
-            }
-        }
-        __syncthreads();  // (the next part starts with buffer 0 again)
     }
+    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const uint32_t es = s == 0 ? E.x : s == 1 ? E.y : s == 2 ? E.z : E.w;
+        const uint32_t byte = (es >> (8 * g)) & 255u;
+        if constexpr (X4) {
+            const i32x8 a8 = {(int)C[s].x, (int)C[s].y, (int)C[s].z, (int)C[s].w, 0, 0, 0, 0};
+            const i32x8 b8 = {(int)Xv[s].x, (int)Xv[s].y, (int)Xv[s].z, (int)Xv[s].w, 0, 0, 0, 0};
+            acc[s & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, acc[s & 1], 4, 4, 0, (int)byte, 0,
+                                                                          (int)xe[s]);
+        } else {
+            const float f = mx4_scale(byte);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t d = j == 0 ? C[s].x : j == 1 ? C[s].y : j == 2 ? C[s].z : C[s].w;
+                acc[j & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, widen_mx4(d, f)), __builtin_bit_cast(bf16x8, Xv[4 * s + j]),
+                    acc[j & 1], 0, 0, 0);
+            }
+        }
+    }
+    red[wv][lane] = acc[0] + acc[1];
+    __syncthreads();
+    const int t = threadIdx.x >> 4, r = threadIdx.x & 15;  // token, row
+    if (t >= T || r0 + r >= N) return;
+    const int l = t + 16 * (r >> 2);  // D lane layout: column t, element r % 4
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsWaves; ++w) v += ((const float*)&red[w][l])[r & 3];
+    mt.y[(int64_t)t * N + r0 + r] = v;
 }
 
 // Block -> (K part, row tile over the matrices of the set, token tile).  Blocks are dealt to
@@ -889,13 +867,10 @@ hipError_t launch_gemm16(const Mx4Launch& l) {
 
 hipError_t launch_rows(const Mx4Launch& l) {
     int rt = 0;
-    const GemmMats gm = gemm_mats(l.mats, l.wscales, l.n, 16, l.parts, &rt);
-    const int parts = (int)((l.d_in + kRowsK - 1) / kRowsK);
-    // two blocks per CU, every block the same number of tiles
-    const int rounds = (rt * l.S + 511) / 512;
-    const dim3 grid((unsigned)((rt + rounds - 1) / rounds), (unsigned)l.S), block(64 * kRowsWaves);
-    if (l.xscales) k_mx4_rows<true><<<grid, block, 0, l.s>>>(l.x, l.xscales, gm, (int)l.T, (int)l.d_in, parts);
-    else k_mx4_rows<false><<<grid, block, 0, l.s>>>(l.x, nullptr, gm, (int)l.T, (int)l.d_in, parts);
+    const GemmMats gm = gemm_mats(l.mats, l.wscales, l.n, 16, nullptr, &rt);
+    const dim3 grid((unsigned)rt), block(64 * kRowsWaves);
+    if (l.xscales) k_mx4_rows<true><<<grid, block, 0, l.s>>>(l.x, l.xscales, gm, (int)l.T, (int)l.d_in);
+    else k_mx4_rows<false><<<grid, block, 0, l.s>>>(l.x, nullptr, gm, (int)l.T, (int)l.d_in);
     return hipGetLastError();
 }
 
@@ -933,7 +908,7 @@ struct TileCost {
     int tile, br, bt, occ;
     double a, b, c;
 };
-enum { k256x256, k128x256, k128x128, k128x64, k128x32, k64x64, k64x32 };
+enum { kRows, k256x256, k128x256, k128x128, k128x64, k128x32, k64x64, k64x32 };
 constexpr TileCost kCost4[] = {{k256x256, 256, 256, 1, 7.7, 0.0, 1.60},
                                {k128x256, 128, 256, 1, 4.9, 0.0, 1.09},
                                {k128x128, 128, 128, 1, 5.1, 0.0, 0.655},
@@ -949,13 +924,13 @@ struct Mx4Plan {
     int64_t kps;
 };
 Mx4Plan plan_mx4(bool x4, int64_t T, int64_t d_in, const int64_t* d_outs, int n, bool split_ok) {
-    Mx4Plan pl = {0, 1, d_in};
-    if (T <= kRowsMaxT) {
-        if (split_ok && d_in > kRowsK) pl = {0, (int)((d_in + kRowsK - 1) / kRowsK), kRowsK};
-        return pl;
+    Mx4Plan pl = {kRows, 1, d_in};
+    int64_t N = 0, tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        N += d_outs[i];
+        tiles += (d_outs[i] + 15) / 16;
     }
-    int64_t N = 0;
-    for (int i = 0; i < n; ++i) N += d_outs[i];
+    if (rows_fit(x4, T, d_in, tiles)) return pl;
     double best = 1e30;
     for (int k = 0; k < 5; ++k) {
         const TileCost& t = x4 ? kCost4[k] : kCost16[k];
@@ -1008,7 +983,7 @@ hipError_t launch_mx4_product(const void* x, const uint8_t* xscales, int64_t T, 
     }
     const Mx4Launch l = {x, xscales, T, d_in, mats, wscales, n, pl.S, pl.kps, pl.S > 1 ? parts : nullptr, s};
     hipError_t e;
-    if (T <= kRowsMaxT) {
+    if (pl.tile == kRows) {
         e = launch_rows(l);
     } else if (xscales) {
         switch (pl.tile) {
