@@ -317,23 +317,24 @@ k_mx4_rows(const void* __restrict__ x, const uint8_t* __restrict__ xs, const Gem
 }
 
 // Block -> (K part, row tile over the matrices of the set, token tile).  Blocks are dealt to
-// the 8 XCDs in turn: XCD id % 8 takes the row tiles congruent to it, GR of them at a time
-// (the last group what is left) with all token tiles, so that the blocks an XCD runs
-// together share both operands' tiles in its L2.
+// the 8 XCDs in turn (id % 8); each XCD takes an equal run of the tiles, in an order that
+// walks GR row tiles (the last group what is left) with all token tiles, so that the blocks
+// an XCD runs together share both operands' tiles in its L2.  rt: nrt past the last tile.
 struct TileId {
     int sp, rt, tt;
 };
-__device__ __forceinline__ TileId tile_id(int ntt, int S, int GR) {
-    const int per = (int)(gridDim.x / (unsigned)S), nr = per / (8 * ntt);  // row tiles of an XCD
+__device__ __forceinline__ TileId tile_id(int nrt, int ntt, int S, int GR) {
+    const int per = (int)(gridDim.x / (unsigned)S);
     TileId t;
     t.sp = (int)blockIdx.x / per;
     const int id = (int)blockIdx.x - t.sp * per;
-    const int q = id >> 3, g = q / (GR * ntt), rem = q - g * (GR * ntt);
-    const int gs = nr - g * GR < GR ? nr - g * GR : GR;  // row tiles of this group
-    t.tt = rem / gs;
-    t.rt = (g * GR + rem - t.tt * gs) * 8 + (id & 7);
+    const int lin = (id & 7) * (per >> 3) + (id >> 3), g = lin / (GR * ntt), rem = lin - g * (GR * ntt);
+    const int gs = nrt - g * GR < GR ? nrt - g * GR : GR;  // row tiles of this group
+    t.tt = gs > 0 ? rem / gs : ntt;
+    t.rt = t.tt < ntt ? g * GR + rem - t.tt * gs : nrt;
     return t;
 }
+inline unsigned tile_grid(int nrt, int ntt, int S) { return (unsigned)((nrt * ntt + 7) / 8 * 8 * S); }
 
 // The product on MX4 tokens for batches of many tokens: block tiles of BR rows of Wq x BT
 // tokens, NWR x NWT waves, each a block of MI x NJ tiles of the block-scaled
@@ -364,7 +365,7 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
     static_assert(NS >= 3, "a stage's copies go out between the products of an earlier one");
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char* const sring = smem + NS * kStageBytes;
-    const TileId tid = tile_id(ntt, S, GR);
+    const TileId tid = tile_id(gm.rt_begin[gm.n], ntt, S, GR);
     const int sp = tid.sp, rtg = tid.rt, tt = tid.tt;
     if (rtg >= gm.rt_begin[gm.n]) return;  // uniform
     BD_MAT_OF(mt, gm, rtg);
@@ -450,15 +451,12 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
     const int m32 = lane & 31, h = lane >> 5;
     int sa[2][MI], sb[2][NJ];          // a stage's scales, by its parity
     u32x4 A[2][MI], Bv[2][NJ];         // a step's operands, by its parity (kSteps is even)
-    auto read = [&](int s, auto kc) {  // step kk of stage s: chunk kSteps h + kk of the wave's rows
+    // operand r of step kk of stage s (chunk kSteps h + kk of 32 rows): MI of W, then NJ tokens'
+    auto read = [&](int s, auto kc, int r) {
         constexpr int kk = decltype(kc)::value;
-        const char* wt_base = smem + (s % NS) * kStageBytes + wr * (BR / NWR) * kRowB;
-        const char* xt_base = smem + (s % NS) * kStageBytes + (BR + wt * (BT / NWT)) * kRowB;
-        const int off = m32 * kRowB + 16 * ((kSteps * h + kk) ^ swz(m32));
-#pragma unroll
-        for (int i = 0; i < MI; ++i) A[kk & 1][i] = *(const u32x4*)(wt_base + off + 32 * kRowB * i);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) Bv[kk & 1][j] = *(const u32x4*)(xt_base + off + 32 * kRowB * j);
+        const char* base = smem + (s % NS) * kStageBytes + m32 * kRowB + 16 * ((kSteps * h + kk) ^ swz(m32));
+        if (r < MI) A[kk & 1][r < MI ? r : 0] = *(const u32x4*)(base + (wr * (BR / NWR) + 32 * r) * kRowB);
+        else Bv[kk & 1][r < MI ? 0 : r - MI] = *(const u32x4*)(base + (BR + wt * (BT / NWT) + 32 * (r - MI)) * kRowB);
     };
     auto read_scales = [&](int s, auto jc) {  // s % P == J
         constexpr int J = decltype(jc)::value % P, O = J & 1;
@@ -469,35 +467,40 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
 #pragma unroll
         for (int j = 0; j < NJ; ++j) sb[O][j] = (int)*(const ST*)(sc + (BR + wt * (BT / NWT) + 32 * j) * 16);
     };
-    // Step kk's products, with stage s's share of copies between them: stage s sends out the
-    // copies of stage s + NS - 1, and a period's first stage before them the scales of the
-    // next period, spread evenly over its products.  (All at once, behind the barrier, the
-    // copies hold up every wave's products while the address unit takes them in turn.)
-    auto products = [&](int s, auto kc, auto jc) {
+    // Step kk's products; between them the reads of the next step (sn, nc)'s operands and stage
+    // s's share of copies: stage s sends out the copies of stage s + NS - 1, and a period's
+    // first stage before them the scales of the next period, spread evenly over its products.
+    // (All at once, copies or reads hold up every wave's products while the address unit or
+    // the LDS takes them in turn: 256 columns of a 256 x 256 block took 3600 cycles with the
+    // copies behind the barrier, 3250 with the reads alone in bursts.)
+    auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
         constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
         constexpr int kS = J == 0 ? kSInst : 0, kTot = kS + kD, M = kSteps * MI * NJ;
-        __builtin_amdgcn_sched_barrier(0);  // the reads before stay ahead of the products
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const u32x4 v = A[kk & 1][i];
             const i32x8 a8 = {(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const int q = kk * MI * NJ + i * NJ + j;  // this product of the stage's M
+                const int ql = i * NJ + j, q = kk * MI * NJ + ql;  // this product of the step, of the stage
+#pragma unroll
+                for (int r = 0; r < MI + NJ; ++r)
+                    if (r * MI * NJ / (MI + NJ) == ql) read(sn, nc, r);
 #pragma unroll
                 for (int c = 0; c < kTot; ++c) {
                     if (c * M / kTot != q) continue;
                     if (c < kS) copy_scales(s / P + 1, c < kS ? c : 0);
                     else copy(s + NS - 1, c - kS);
-                    __builtin_amdgcn_sched_barrier(0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 const u32x4 w = Bv[kk & 1][j];
                 const i32x8 b8 = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[i][j], 4, 4, kk, sb[O][j],
                                                                             kk, sa[O][i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
     };
     using C0 = std::integral_constant<int, 0>;
     using C1 = std::integral_constant<int, 1>;
@@ -508,13 +511,10 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
     // slot and, after the wait, shows stage s + 1.
     auto stage = [&](int s, auto jc) {  // s % P == J
         constexpr int J = decltype(jc)::value;
-        read(s, C1());
-        products(s, C0(), jc);
+        products(s, C0(), jc, s, C1());
         if constexpr (kSteps == 4) {
-            read(s, C2());
-            products(s, C1(), jc);
-            read(s, C3());
-            products(s, C2(), jc);
+            products(s, C1(), jc, s, C2());
+            products(s, C2(), jc, s, C3());
         }
         // in flight beyond what stage s + 1 needs: this stage's copies so far and those of the
         // NS - 3 stages before it, except scales that stage s + 1 starts on
@@ -535,13 +535,13 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
         wait_vmcnt_lgkm<pending>();
         __builtin_amdgcn_s_barrier();
         read_scales(s + 1, std::integral_constant<int, J + 1>());
-        read(s + 1, C0());
-        products(s, std::integral_constant<int, kSteps - 1>(), jc);
+        products(s, std::integral_constant<int, kSteps - 1>(), jc, s + 1, C0());
     };
     wait_vmcnt<(NS - 2) * kD>();
     __builtin_amdgcn_s_barrier();
     read_scales(0, C0());
-    read(0, C0());
+#pragma unroll
+    for (int r = 0; r < MI + NJ; ++r) read(0, C0(), r);
     for (int s = 0; s < nk; s += P) {  // (uniform branches)
         stage(s, C0());
         if (s + 1 < nk) stage(s + 1, C1());
@@ -581,7 +581,7 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
     extern __shared__ __attribute__((aligned(16))) char smem[];
     char* const wring = smem + NSX * kXSlot;
     char* const sring = wring + NSW * kWSlot;
-    const TileId tid = tile_id(ntt, S, GR);
+    const TileId tid = tile_id(gm.rt_begin[gm.n], ntt, S, GR);
     const int sp = tid.sp, rtg = tid.rt, tt = tid.tt;
     if (rtg >= gm.rt_begin[gm.n]) return;  // uniform
     BD_MAT_OF(mt, gm, rtg);
@@ -662,12 +662,10 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
     u32x4 C[2][MI];  // a stage's codes and scales, by its parity
     float f[2][MI];
     u32x4 Bv[2][NJ];  // a step's tokens, by its parity
-    auto read_x = [&](int s, auto kc) {  // step kk of stage s: chunk 4 h + kk of the wave's tokens
+    auto read_x = [&](int s, auto kc, int j) {  // step kk of stage s: chunk 4 h + kk of token tile j
         constexpr int kk = decltype(kc)::value;
-        const char* xt = smem + (s % NSX) * kXSlot + wt * (BT / NWT) * 128 + m32 * 128 +
-                         16 * ((4 * h + kk) ^ ((m32 / 2) % 8));
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) Bv[kk & 1][j] = *(const u32x4*)(xt + 4096 * j);
+        Bv[kk & 1][j] = *(const u32x4*)(smem + (s % NSX) * kXSlot + (wt * (BT / NWT) + 32 * j + m32) * 128 +
+                                        16 * ((4 * h + kk) ^ ((m32 / 2) % 8)));
     };
     auto read_w = [&](int s, auto jc) {  // s % 8 == J: block 2 (J % kSpW) + h of the wave's rows
         constexpr int J = decltype(jc)::value % 8, O = J & 1;
@@ -680,23 +678,25 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
             f[O][i] = mx4_scale(*(const uint8_t*)(sc + 512 * i));
         }
     };
-    // Step kk's products with stage s's share of copies between them: stage s sends out the
-    // tokens of stage s + NSX - 1 and before them, in a slot's first stage, the codes NSW - 1
-    // slots on and, in a period's first, the next period's scales.
-    auto products = [&](int s, auto kc, auto jc) {
+    // Step kk's products; between them the reads of the next step (sn, nc)'s tokens and stage
+    // s's share of copies, as in k_mx4_gemm4: stage s sends out the tokens of stage
+    // s + NSX - 1 and before them, in a slot's first stage, the codes NSW - 1 slots on and,
+    // in a period's first, the next period's scales.
+    auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
         constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
         constexpr int kS = J == 0 ? kSInst : 0, kW = J % kSpW == 0 ? kWInst : 0;
         constexpr int kTot = kS + kW + kXInst, M = 4 * MI * NJ;
-        __builtin_amdgcn_sched_barrier(0);  // the reads before stay ahead of the products
-        u32x4 A[MI];
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-            A[i] = widen_mx4(kk == 0 ? C[O][i].x : kk == 1 ? C[O][i].y : kk == 2 ? C[O][i].z : C[O][i].w, f[O][i]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
+            const u32x4 A =
+                widen_mx4(kk == 0 ? C[O][i].x : kk == 1 ? C[O][i].y : kk == 2 ? C[O][i].z : C[O][i].w, f[O][i]);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const int q = kk * MI * NJ + i * NJ + j;  // this product of the stage's M
+                const int ql = i * NJ + j, q = kk * MI * NJ + ql;  // this product of the step, of the stage
+#pragma unroll
+                for (int r = 0; r < NJ; ++r)
+                    if (r * MI == ql) read_x(sn, nc, r);
 #pragma unroll
                 for (int c = 0; c < kTot; ++c) {
                     if (c * M / kTot != q) continue;
@@ -704,8 +704,10 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
                     else if (c < kS + kW) copy_w(s / kSpW + NSW - 1, c < kS + kW ? c - kS : 0);
                     else copy_x(s + NSX - 1, c - kS - kW);
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, Bv[kk & 1][j]), __builtin_bit_cast(bf16x8, A[i]), acc[i][j], 0, 0, 0);
+                    __builtin_bit_cast(bf16x8, Bv[kk & 1][j]), __builtin_bit_cast(bf16x8, A), acc[i][j], 0, 0, 0);
+                if (j + 1 < NJ) __builtin_amdgcn_sched_barrier(0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -716,12 +718,9 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
     using C3 = std::integral_constant<int, 3>;
     auto stage = [&](int s, auto jc) {  // s % 8 == J
         constexpr int J = decltype(jc)::value;
-        read_x(s, C1());
-        products(s, C0(), jc);
-        read_x(s, C2());
-        products(s, C1(), jc);
-        read_x(s, C3());
-        products(s, C2(), jc);
+        products(s, C0(), jc, s, C1());
+        products(s, C1(), jc, s, C2());
+        products(s, C2(), jc, s, C3());
         // in flight beyond what stage s + 1 needs: this stage's copies so far and those of the
         // NSX - 3 stages before it (its codes and scales went out no later than its tokens)
         constexpr auto pending = [] {
@@ -741,13 +740,13 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
         wait_vmcnt_lgkm<pending>();
         __builtin_amdgcn_s_barrier();
         read_w(s + 1, std::integral_constant<int, J + 1>());
-        read_x(s + 1, C0());
-        products(s, C3(), jc);
+        products(s, C3(), jc, s + 1, C0());
     };
     wait_vmcnt<(NSX - 2) * kXInst>();
     __builtin_amdgcn_s_barrier();
     read_w(0, C0());
-    read_x(0, C0());
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) read_x(0, C0(), j);
     for (int s = 0; s < nk; s += 8) {  // (uniform branches)
         stage(s, std::integral_constant<int, 0>());
         if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>());
@@ -846,7 +845,7 @@ hipError_t launch_gemm4(const Mx4Launch& l) {
     int rt = 0;
     const GemmMats gm = gemm_mats(l.mats, l.wscales, l.n, BR, l.parts, &rt);
     const int ntt = (int)((l.T + BT - 1) / BT), GR = row_group(ntt);
-    const unsigned blocks = (unsigned)((rt + 7) / 8 * 8 * ntt * l.S);
+    const unsigned blocks = tile_grid(rt, ntt, l.S);
     constexpr int lds = (BR + BT) * NS * (KC / 2) + (BR + BT + 63) / 64 * 64 * 32;
     k_mx4_gemm4<BR, BT, KC, NS, NWR, NWT><<<dim3(blocks), dim3(64 * NWR * NWT), lds, l.s>>>(
         (const uint8_t*)l.x, l.xscales, gm, (int)l.T, (int)l.d_in, ntt, l.S, (int)l.kps, GR);
@@ -858,7 +857,7 @@ hipError_t launch_gemm16(const Mx4Launch& l) {
     int rt = 0;
     const GemmMats gm = gemm_mats(l.mats, l.wscales, l.n, BR, l.parts, &rt);
     const int ntt = (int)((l.T + BT - 1) / BT), GR = row_group(ntt);
-    const unsigned blocks = (unsigned)((rt + 7) / 8 * 8 * ntt * l.S);
+    const unsigned blocks = tile_grid(rt, ntt, l.S);
     constexpr int lds = NSX * BT * 128 + NSW * BR * (WC / 2) + 2 * BR * 16;
     k_mx4_gemm16<BR, BT, WC, NSX, NSW, NWR, NWT><<<dim3(blocks), dim3(64 * NWR * NWT), lds, l.s>>>(
         (const uint16_t*)l.x, gm, (int)l.T, (int)l.d_in, ntt, l.S, (int)l.kps, GR);
