@@ -71,94 +71,186 @@ __device__ __forceinline__ f32x4 mfma_f6f4(i32x6 a, u32x4 b, f32x4 c, uint32_t s
 }  // namespace
 
 // ------------------------------------------------------------ tile packing
-// The work items of k_group (runs of <= 32 positions of one user, in position
-// order) are packed into tiles of <= 16 positions: an item of c <= 16 positions
+// The work items (runs of <= 32 positions of one user, in position order; made here from the
+// sorted users, or by k_group_wave) are packed into tiles of <= 16 positions: an item of c <= 16 positions
 // joins the open tile if it fits and otherwise starts a new one (so a user of at
 // most 16 tokens is never split); an item of 17..32 starts a tile of 16 and opens
 // one with the rest.  Every tile but the last, together with the next, holds more
-// than 16 positions: at most 2 ceil(T / 16) + 1 tiles.  One wave: the open tile's
-// length is a short serial recurrence over the items (scalar, 64 per round); the
-// tile starts are then written by the items' lanes.  tiles[t] = first position of
+// than 16 positions: at most 2 ceil(T / 16) + 1 tiles.  tiles[t] = first position of
 // tile t, tiles[ntiles] = number of valid positions, meta[3] = ntiles.
 // The delta kernel's cost of a tile grows with its number of distinct users (one
 // product pass and one bank stream per user), so the tiles are also listed by that
-// number, largest first (torder, a counting sort, stable within a count): the grid
+// number, largest first (torder, stable within a count): the grid
 // starts the longest blocks first and the short ones fill the end.
-constexpr int kMaxTilesLds = 2 * (kMaxGroupT / 16) + 1;
-__global__ void __launch_bounds__(64)
-k_tile_plan(const int4* __restrict__ items, const int32_t* __restrict__ suser,
+constexpr int kPlanThreads = 1024;
+// Exclusive scans over the block's NW waves (sc: one word per wave): the sum of the threads
+// before, or their maximum (0 for none; values >= 0).
+template <int NW, bool MAX>
+__device__ __forceinline__ int block_scan(int v, int32_t* sc, int* total) {
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(incl, off);
+        if (l >= off) incl = MAX ? (incl > o ? incl : o) : incl + o;
+    }
+    __syncthreads();  // (sc's readers of an earlier scan)
+    if (l == 63) sc[w] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll 1
+    for (int q = 0; q < NW; ++q) {
+        const int o = sc[q];
+        if (q < w) before = MAX ? (before > o ? before : o) : before + o;
+        all = MAX ? (all > o ? all : o) : all + o;
+    }
+    if (total) *total = all;
+    int excl = __shfl_up(incl, 1);
+    if (l == 0) excl = 0;
+    return MAX ? (before > excl ? before : excl) : before + excl;
+}
+
+// ITEMS: the block (kPlanThreads threads) first cuts the sorted users into the work items;
+// otherwise one wave takes them from k_group_wave.  The loops stay rolled and work on LDS: a
+// kernel that runs once, on one CU, waits for its instructions as much as for its data
+// (unrolled to 6.4 KB with its loads in flight it took as long, 14 us, as with loads in turn).
+template <bool ITEMS>
+__global__ void __launch_bounds__(ITEMS ? kPlanThreads : 64)
+k_tile_plan(int4* __restrict__ items, const int32_t* __restrict__ suser,
             uint32_t* __restrict__ meta, int32_t* __restrict__ tiles,
             int32_t* __restrict__ torder, int32_t* __restrict__ tpre, int maxt) {
-    __shared__ int32_t st[kMaxTilesLds + 1];
-    __shared__ uint8_t snu[kMaxTilesLds];
-    const int lane = threadIdx.x;
-    const int nit = (int)meta[1];
-    int cl = 0, nt = 0;  // open tile length, tiles started (uniform)
-    for (int b = 0; b < nit; b += 64) {
-        const int4 it = b + lane < nit ? items[b + lane] : make_int4(0, 0, 0, 0);
-        const int m = nit - b < 64 ? nit - b : 64;
-        uint64_t smask = 0;  // item k starts a tile
-        for (int k = 0; k < m; ++k) {
-            const int c = __builtin_amdgcn_readlane(it.z, k);
-            const int c0 = c > 16 ? 16 : c;
-            const bool stt = cl == 0 || cl + c0 > 16;
-            smask |= (uint64_t)stt << k;
-            cl = c > 16 ? c - 16 : (stt ? c : cl + c);
-        }
-        const bool stt = (smask >> lane) & 1ull;
-        const bool big = lane < m && it.z > 16;
-        const uint64_t bmask = __ballot(big);
-        const uint64_t below = (1ull << lane) - 1ull;
-        const int idx = nt + __popcll(smask & below) + __popcll(bmask & below);
-        if (lane < m) {
-            if (stt && idx < maxt) {
-                tiles[idx] = it.y;
-                st[idx] = it.y;
+    constexpr int kThreads = ITEMS ? kPlanThreads : 64, kMaxT = ITEMS ? kMaxGroupT : kGroupWaveT;
+    constexpr int kMaxTiles = 2 * ((kMaxT + 15) / 16) + 1;
+    __shared__ int32_t su[kMaxT + 1];        // su[p + 1]: the user of sorted position p
+    __shared__ uint16_t ist[kMaxT + 1];      // the items' first positions
+    __shared__ int32_t st[kMaxTiles + 1];
+    __shared__ uint8_t snu[kMaxTiles];
+    __shared__ uint16_t jump[2][kMaxT + 1];  // item -> the next tile start, and 2, 4, .. starts on
+    __shared__ uint8_t hit[kMaxT + 1];       // the item starts a tile
+    __shared__ int32_t sc[kThreads / 64];
+    const int tid = threadIdx.x;
+    const int nv = (int)meta[2];
+    if (tid == 0) su[0] = -1;
+    for (int p = tid; p < nv; p += kThreads) su[p + 1] = suser[p];
+    int nit;
+    if constexpr (ITEMS) {
+        __syncthreads();
+        // thread t takes positions [lo, hi); a position starts an item if it is a multiple of
+        // kItemTokens from its user's first (seg: that position plus 1, of the open user)
+        const int per = (nv + kPlanThreads - 1) / kPlanThreads;
+        const int lo = tid * per < nv ? tid * per : nv, hi = lo + per < nv ? lo + per : nv;
+        int last = 0;
+#pragma unroll 1
+        for (int p = lo; p < hi; ++p)
+            if (su[p + 1] != su[p]) last = p + 1;
+        int seg = block_scan<kThreads / 64, true>(last, sc, nullptr), cnt = 0;
+        uint32_t starts = 0;
+#pragma unroll 1
+        for (int p = lo; p < hi; ++p) {
+            if (su[p + 1] != su[p]) seg = p + 1;
+            if ((p + 1 - seg) % kItemTokens == 0) {
+                starts |= 1u << (p - lo);
+                ++cnt;
             }
-            if (big && idx + (int)stt < maxt) {
-                tiles[idx + (int)stt] = it.y + 16;
-                st[idx + (int)stt] = it.y + 16;
-            }
         }
-        nt += __popcll(smask) + __popcll(bmask);
+        int to = block_scan<kThreads / 64, false>(cnt, sc, &nit);
+#pragma unroll 1
+        for (; starts; starts &= starts - 1u) ist[to++] = (uint16_t)(lo + __ffs((int)starts) - 1);
+        if (tid == 0) {
+            ist[nit] = (uint16_t)nv;
+            meta[1] = (uint32_t)nit;
+        }
+        __syncthreads();
+        for (int k = tid; k < nit; k += kPlanThreads)
+            items[k] = make_int4(su[ist[k] + 1], ist[k], ist[k + 1] - ist[k], 0);
+    } else {
+        nit = (int)meta[1];
+    }
+    // An item that starts a tile leaves it with its count (or, above 16, opens the next with the
+    // rest); the next start is the first item after it that does not fit, at most 16 items on.
+    // The starts are the items reached from item 0, marked by doubling the jumps: one item after
+    // the other, on a lane's broadcasts, took 155 cycles an item.
+    for (int k = tid; k < nit; k += kThreads) {
+        if constexpr (!ITEMS) ist[k] = (uint16_t)items[k].y;
+        hit[k] = k == 0 ? 1 : 0;
+    }
+    if (!ITEMS && tid == 0) ist[nit] = (uint16_t)nv;
+    __syncthreads();
+    for (int k = tid; k < nit; k += kThreads) {
+        const int c = ist[k + 1] - ist[k];
+        int cl = c > 16 ? c - 16 : c, j = k + 1;
+#pragma unroll 1
+        for (; j < nit; ++j) {
+            const int cj = ist[j + 1] - ist[j];
+            if (cl + cj > 16) break;
+            cl += cj;
+        }
+        jump[0][k] = (uint16_t)j;
+    }
+    if (tid == 0) jump[0][nit] = jump[1][nit] = (uint16_t)nit;
+    __syncthreads();
+    int cur = 0;
+#pragma unroll 1
+    for (int reach = 1; reach < nit; reach *= 2, cur ^= 1) {
+        for (int k = tid; k < nit; k += kThreads) {
+            const int j = jump[cur][k];
+            if (hit[k]) hit[j] = 1;  // (also marks made in this round: items reached either way)
+            jump[cur ^ 1][k] = jump[cur][j];
+        }
+        __syncthreads();
+    }
+    // thread t takes items [k0, k1): its tiles follow those of the items before
+    const int per = (nit + kThreads - 1) / kThreads;
+    const int k0 = tid * per < nit ? tid * per : nit, k1 = k0 + per < nit ? k0 + per : nit;
+    int mine = 0, nt;
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k) mine += hit[k] + (ist[k + 1] - ist[k] > 16 ? 1 : 0);
+    int at = block_scan<kThreads / 64, false>(mine, sc, &nt);
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k) {
+        const int p = ist[k];
+        if (hit[k]) {
+            if (at < maxt) tiles[at] = st[at] = p;
+            ++at;
+        }
+        if (ist[k + 1] - p > 16) {
+            if (at < maxt) tiles[at] = st[at] = p + 16;
+            ++at;
+        }
     }
     nt = nt < maxt ? nt : maxt;
-    const int nv = (int)meta[2];
-    if (lane == 0) {
+    if (tid == 0) {
         tiles[nt] = nv;
         st[nt] = nv;
         meta[3] = (uint32_t)nt;
     }
     __syncthreads();
     // distinct users of each tile: user changes over its (sorted) positions
-    for (int t = lane; t < nt; t += 64) {
+    for (int t = tid; t < nt; t += kThreads) {
         const int a = st[t], e = st[t + 1];
-        int cnt = 0, prev = -1;
-        for (int q = a; q < e; ++q) {
-            const int u = suser[q];
-            cnt += u != prev;
-            prev = u;
-        }
+        int cnt = 0;
+#pragma unroll 1
+        for (int q = a; q < e; ++q) cnt += q == a || su[q + 1] != su[q] ? 1 : 0;
         snu[t] = (uint8_t)cnt;
     }
     __syncthreads();
-    // tpre[k]: the users of the tiles of rank < k (their sum in tpre[nt])
-    int pos = 0, pre = 0;
-    for (int v = 16; v >= 0; --v) {  // (a tile holds 1..16 positions; 0 keeps every tile ranked)
-        for (int b = 0; b < nt; b += 64) {
-            const int t = b + lane;
-            const bool hit = t < nt && snu[t] == v;
-            const uint64_t mk = __ballot(hit);
-            const int below = __popcll(mk & ((1ull << lane) - 1ull));
-            if (hit) {
-                torder[pos + below] = t;
-                tpre[pos + below] = pre + v * below;
-            }
-            pos += __popcll(mk);
-            pre += v * __popcll(mk);
+    // a tile's rank: the tiles with more users, and those with as many before it; tpre[k]: the
+    // users of the tiles of rank < k (their sum in tpre[nt])
+    for (int t = tid; t < nt; t += kThreads) {
+        const int v = snu[t];
+        int rank = 0, pre = 0;
+#pragma unroll 4
+        for (int q = 0; q < nt; ++q) {
+            const int o = snu[q];
+            const bool before = o > v || (o == v && q < t);
+            rank += before ? 1 : 0;
+            pre += before ? o : 0;
         }
+        torder[rank] = t;
+        tpre[rank] = pre;
+        if (rank == nt - 1) tpre[nt] = pre + v;
     }
-    if (lane == 0) tpre[nt] = pre;
+    if (tid == 0 && nt == 0) tpre[0] = 0;
 }
 
 // ------------------------------------------------------------ tile encoding
@@ -1327,10 +1419,17 @@ k_delta8(const DeltaMats dm, const int32_t* __restrict__ tmeta,
 // ---------------------------------------------------------------- host side
 hipError_t launch_tile_plan(const BatchPlan& bp, char* batch, hipStream_t s) {
     if (bp.xdtype != BD_BF16 || bp.T == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_tile_plan, dim3(1), dim3(64), 0, s, (const int4*)(batch + bp.off_items),
-                       (const int32_t*)(batch + bp.off_user), (uint32_t*)(batch + bp.off_meta),
-                       (int32_t*)(batch + bp.off_tiles), (int32_t*)(batch + bp.off_torder),
-                       (int32_t*)(batch + bp.off_tpre), (int)bp.ntiles);
+    int4* items = (int4*)(batch + bp.off_items);
+    const int32_t* suser = (const int32_t*)(batch + bp.off_user);
+    uint32_t* meta = (uint32_t*)(batch + bp.off_meta);
+    int32_t *tiles = (int32_t*)(batch + bp.off_tiles), *torder = (int32_t*)(batch + bp.off_torder),
+            *tpre = (int32_t*)(batch + bp.off_tpre);
+    if (bp.T > kGroupWaveT)
+        k_tile_plan<true><<<dim3(1), dim3(kPlanThreads), 0, s>>>(items, suser, meta, tiles, torder, tpre,
+                                                                 (int)bp.ntiles);
+    else
+        k_tile_plan<false><<<dim3(1), dim3(64), 0, s>>>(items, suser, meta, tiles, torder, tpre,
+                                                        (int)bp.ntiles);
     return hipGetLastError();
 }
 

@@ -68,7 +68,8 @@ hipError_t launch_select_axis(const AxisPlan& ap, const void* wf, const void* wb
 // ------------------------------------------------------------------- apply
 constexpr int kItemTokens = 32;   // max tokens of one (user, chunk) work item (<= 2 MFMA tiles)
 constexpr int kMaxMats = 4;       // matrices of one grouped launch (they share X)
-constexpr int kMaxGroupT = 8192;  // tokens the one-block grouping kernel sorts in LDS
+constexpr int kMaxGroupT = 8192;  // tokens of a prepared batch
+constexpr int kGroupWaveT = 64;   // ... that one wave groups and cuts into items (k_group_wave)
 constexpr int kMaxUsers = (1 << 17) - 1;
 
 // Prepared batch (bd_batch_prepare): tokens grouped by user into work items; for
