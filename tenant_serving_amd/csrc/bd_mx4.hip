@@ -561,7 +561,12 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
 // a time (WC / 2 bytes a row) into a ring of NSW slots, the scales 512 columns at a time
 // into two slots.  Lane half h takes block h (32 columns) of a stage: 16 bytes of codes and
 // one scale per row serve its four steps, step kk columns 8 kk .. 8 kk + 7 of the block.
-template <int BR, int BT, int WC, int NSX, int NSW, int NWR, int NWT>
+// WHOLE: a stage's operands are all read during the stage before (their registers are few for
+// tiles of 32 and 64 tokens), so that no product waits for the LDS: 28672 x 4096 at 16 tokens
+// 18.8 -> 16.7 us, at 128 tokens 38 -> 36, 4096 x 4096 at 64 tokens 11.2 -> 10.5 (the 128 x 128
+// tile, whose larger ring then leaves two blocks to a CU no more slack, 188 -> 196 us on
+// 5120 x 17408 at 1144 tokens, stays with the step before).
+template <int BR, int BT, int WC, int NSX, int NSW, int NWR, int NWT, bool WHOLE>
 __global__ void __launch_bounds__(64 * NWR * NWT)
 k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, int ntt, int S,
              int kps, int GR) {
@@ -575,7 +580,7 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
     static_assert(BT % (8 * NW) == 0 && kWSlot % (1024 * NW) == 0 && BR % 64 == 0,
                   "whole copy instructions per wave");
     static_assert(MI >= 1 && NJ >= 1 && BR % (32 * NWR) == 0 && BT % (32 * NWT) == 0, "32 x 32 tiles");
-    static_assert(NSX >= 3 && (NSW - 1) * kSpW >= NSX - 1 && NSX <= 8 && 8 % kSpW == 0,
+    static_assert(NSX >= 3 && (NSW - 1) * kSpW >= NSX - (WHOLE ? 0 : 1) && NSX <= 7 && 8 % kSpW == 0,
                   "a stage's copies go out between the products of an earlier one, its codes and "
                   "scales no later than its tokens");
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -646,116 +651,209 @@ k_mx4_gemm16(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, in
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-    // The prologue: the first period's scales, NSW - 1 slots of codes, NSX - 1 stages of tokens.
-#pragma unroll
-    for (int c = 0; c < kSInst; ++c) copy_s(0, c);
-#pragma unroll
-    for (int u = 0; u < NSW - 1; ++u)
-#pragma unroll
-        for (int c = 0; c < kWInst; ++c) copy_w(u, c);
-#pragma unroll
-    for (int t = 0; t < NSX - 1; ++t)
-#pragma unroll
-        for (int c = 0; c < kXInst; ++c) copy_x(t, c);
-
     const int m32 = lane & 31, h = lane >> 5;
-    u32x4 C[2][MI];  // a stage's codes and scales, by its parity
-    float f[2][MI];
-    u32x4 Bv[2][NJ];  // a step's tokens, by its parity
-    auto read_x = [&](int s, auto kc, int j) {  // step kk of stage s: chunk 4 h + kk of token tile j
-        constexpr int kk = decltype(kc)::value;
-        Bv[kk & 1][j] = *(const u32x4*)(smem + (s % NSX) * kXSlot + (wt * (BT / NWT) + 32 * j + m32) * 128 +
-                                        16 * ((4 * h + kk) ^ ((m32 / 2) % 8)));
-    };
-    auto read_w = [&](int s, auto jc) {  // s % 8 == J: block 2 (J % kSpW) + h of the wave's rows
-        constexpr int J = decltype(jc)::value % 8, O = J & 1;
-        const char* wt_base = wring + ((s / kSpW) % NSW) * kWSlot + wr * (BR / NWR) * kWRow + m32 * kWRow +
-                              16 * ((2 * (J % kSpW) + h) ^ ((m32 / (16 / kWC)) % kWC));
-        const char* sc = sring + ((s >> 3) & 1) * kSSlot + 2 * J + h + 16 * (wr * (BR / NWR) + m32);
+    if constexpr (WHOLE) {
+        // The prologue issues in the loop's order, as if by stages -8 .. -1.
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            C[O][i] = *(const u32x4*)(wt_base + 32 * kWRow * i);
-            f[O][i] = mx4_scale(*(const uint8_t*)(sc + 512 * i));
+        for (int t = -8; t < 0; ++t) {
+            if (t == -8)
+#pragma unroll
+                for (int c = 0; c < kSInst; ++c) copy_s(0, c);
+            if (t % kSpW == 0 && t / kSpW + NSW - 1 >= 0)
+#pragma unroll
+                for (int c = 0; c < kWInst; ++c) copy_w(t / kSpW + NSW - 1, c);
+            if (t + NSX >= 0)
+#pragma unroll
+                for (int c = 0; c < kXInst; ++c) copy_x(t + NSX, c);
         }
-    };
-    // Step kk's products; between them the reads of the next step (sn, nc)'s tokens and stage
-    // s's share of copies, as in k_mx4_gemm4: stage s sends out the tokens of stage
-    // s + NSX - 1 and before them, in a slot's first stage, the codes NSW - 1 slots on and,
-    // in a period's first, the next period's scales.
-    auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
-        constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
-        constexpr int kS = J == 0 ? kSInst : 0, kW = J % kSpW == 0 ? kWInst : 0;
-        constexpr int kTot = kS + kW + kXInst, M = 4 * MI * NJ;
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const u32x4 A =
-                widen_mx4(kk == 0 ? C[O][i].x : kk == 1 ? C[O][i].y : kk == 2 ? C[O][i].z : C[O][i].w, f[O][i]);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int ql = i * NJ + j, q = kk * MI * NJ + ql;  // this product of the step, of the stage
-#pragma unroll
-                for (int r = 0; r < NJ; ++r)
-                    if (r * MI == ql) read_x(sn, nc, r);
-#pragma unroll
-                for (int c = 0; c < kTot; ++c) {
-                    if (c * M / kTot != q) continue;
-                    if (c < kS) copy_s(s / 8 + 1, c < kS ? c : 0);
-                    else if (c < kS + kW) copy_w(s / kSpW + NSW - 1, c < kS + kW ? c - kS : 0);
-                    else copy_x(s + NSX - 1, c - kS - kW);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, Bv[kk & 1][j]), __builtin_bit_cast(bf16x8, A), acc[i][j], 0, 0, 0);
-                if (j + 1 < NJ) __builtin_amdgcn_sched_barrier(0);
+        u32x4 C[2][MI], Bv[2][4][NJ];  // a stage's codes and tokens, by its parity
+        float f[2][MI];
+        constexpr int kReads = MI + 4 * NJ;
+        auto read = [&](int s, auto jc, int r) {  // read r of stage s (s % 8 == J): codes, then tokens
+            constexpr int J = decltype(jc)::value % 8, O = J & 1;
+            if (r < MI) {
+                const int row = wr * (BR / NWR) + 32 * r + m32;
+                C[O][r < MI ? r : 0] =
+                    *(const u32x4*)(wring + ((s / kSpW) % NSW) * kWSlot + row * kWRow +
+                                    16 * ((2 * (J % kSpW) + h) ^ ((m32 / (16 / kWC)) % kWC)));
+                f[O][r < MI ? r : 0] =
+                    mx4_scale(*(const uint8_t*)(sring + ((s >> 3) & 1) * kSSlot + 2 * J + h + 16 * row));
+            } else {
+                const int kk = r < MI ? 0 : (r - MI) / NJ, j = r < MI ? 0 : (r - MI) % NJ;
+                Bv[O][kk][j] = *(const u32x4*)(smem + (s % NSX) * kXSlot + (wt * (BT / NWT) + 32 * j + m32) * 128 +
+                                               16 * ((4 * h + kk) ^ ((m32 / 2) % 8)));
             }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    using C0 = std::integral_constant<int, 0>;
-    using C1 = std::integral_constant<int, 1>;
-    using C2 = std::integral_constant<int, 2>;
-    using C3 = std::integral_constant<int, 3>;
-    auto stage = [&](int s, auto jc) {  // s % 8 == J
-        constexpr int J = decltype(jc)::value;
-        products(s, C0(), jc, s, C1());
-        products(s, C1(), jc, s, C2());
-        products(s, C2(), jc, s, C3());
-        // in flight beyond what stage s + 1 needs: this stage's copies so far and those of the
-        // NSX - 3 stages before it (its codes and scales went out no later than its tokens)
-        constexpr auto pending = [] {
-            int n = 0;
-            for (int d = 0; d <= NSX - 3; ++d) {
-                const int j = (J - d + 8) % 8, M = 4 * MI * NJ;
-                const int kTot = (j == 0 ? kSInst : 0) + (j % kSpW == 0 ? kWInst : 0) + kXInst;
-                int sent = kTot;
-                if (d == 0) {  // the last step's copies are still to come
-                    sent = 0;
-                    for (int c = 0; c < kTot; ++c) sent += c * M / kTot < M - MI * NJ ? 1 : 0;
-                }
-                n += sent;
+        };
+        // in flight behind stage s's tokens, seen from the stage J at whose start they are
+        // needed: what the d = 1 .. n stages before it issued
+        constexpr auto issued = [](int J, int n) {
+            int k = 0;
+            for (int d = 1; d <= n; ++d) {
+                const int j = (J - d + 16) % 8;
+                k += kXInst + (j % kSpW == 0 ? kWInst : 0) + (j == 0 ? kSInst : 0);
             }
-            return n;
-        }();
-        wait_vmcnt_lgkm<pending>();
+            return k;
+        };
+        auto stage = [&](int s, auto jc) {  // s % 8 == J
+            constexpr int J = decltype(jc)::value, O = J & 1;
+            constexpr int kS = J == 0 ? kSInst : 0, kW = J % kSpW == 0 ? kWInst : 0;
+            constexpr int kTot = kS + kW + kXInst, M = 4 * MI * NJ;
+            wait_vmcnt_lgkm<issued(J, NSX - 2)>();  // (and the wave holds stage s: its slot is free)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const u32x4 A =
+                        widen_mx4(kk == 0 ? C[O][i].x : kk == 1 ? C[O][i].y : kk == 2 ? C[O][i].z : C[O][i].w, f[O][i]);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const int q = (kk * MI + i) * NJ + j;
+#pragma unroll
+                        for (int r = 0; r < kReads; ++r)
+                            if (r * M / kReads == q) read(s + 1, std::integral_constant<int, J + 1>(), r);
+#pragma unroll
+                        for (int c = 0; c < kTot; ++c) {
+                            if (c * M / kTot != q) continue;
+                            if (c < kS) copy_s(s / 8 + 1, c < kS ? c : 0);
+                            else if (c < kS + kW) copy_w(s / kSpW + NSW - 1, c < kS + kW ? c - kS : 0);
+                            else copy_x(s + NSX, c - kS - kW);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            __builtin_bit_cast(bf16x8, Bv[O][kk][j]), __builtin_bit_cast(bf16x8, A), acc[i][j], 0, 0, 0);
+                        if (j + 1 < NJ) __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        wait_vmcnt<issued(0, NSX - 1)>();
         __builtin_amdgcn_s_barrier();
-        read_w(s + 1, std::integral_constant<int, J + 1>());
-        products(s, C3(), jc, s + 1, C0());
-    };
-    wait_vmcnt<(NSX - 2) * kXInst>();
-    __builtin_amdgcn_s_barrier();
-    read_w(0, C0());
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) read_x(0, C0(), j);
-    for (int s = 0; s < nk; s += 8) {  // (uniform branches)
-        stage(s, std::integral_constant<int, 0>());
-        if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>());
-        if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>());
-        if (s + 3 < nk) stage(s + 3, std::integral_constant<int, 3>());
-        if (s + 4 < nk) stage(s + 4, std::integral_constant<int, 4>());
-        if (s + 5 < nk) stage(s + 5, std::integral_constant<int, 5>());
-        if (s + 6 < nk) stage(s + 6, std::integral_constant<int, 6>());
-        if (s + 7 < nk) stage(s + 7, std::integral_constant<int, 7>());
+        for (int r = 0; r < kReads; ++r) read(0, std::integral_constant<int, 0>(), r);
+        for (int s = 0; s < nk; s += 8) {  // (uniform branches)
+            stage(s, std::integral_constant<int, 0>());
+            if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>());
+            if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>());
+            if (s + 3 < nk) stage(s + 3, std::integral_constant<int, 3>());
+            if (s + 4 < nk) stage(s + 4, std::integral_constant<int, 4>());
+            if (s + 5 < nk) stage(s + 5, std::integral_constant<int, 5>());
+            if (s + 6 < nk) stage(s + 6, std::integral_constant<int, 6>());
+            if (s + 7 < nk) stage(s + 7, std::integral_constant<int, 7>());
+        }
+    } else {
+        // The prologue: the first period's scales, NSW - 1 slots of codes, NSX - 1 stages of tokens.
+#pragma unroll
+        for (int c = 0; c < kSInst; ++c) copy_s(0, c);
+#pragma unroll
+        for (int u = 0; u < NSW - 1; ++u)
+#pragma unroll
+            for (int c = 0; c < kWInst; ++c) copy_w(u, c);
+#pragma unroll
+        for (int t = 0; t < NSX - 1; ++t)
+#pragma unroll
+            for (int c = 0; c < kXInst; ++c) copy_x(t, c);
+
+        u32x4 C[2][MI];  // a stage's codes and scales, by its parity
+        float f[2][MI];
+        u32x4 Bv[2][NJ];  // a step's tokens, by its parity
+        auto read_x = [&](int s, auto kc, int j) {  // step kk of stage s: chunk 4 h + kk of token tile j
+            constexpr int kk = decltype(kc)::value;
+            Bv[kk & 1][j] = *(const u32x4*)(smem + (s % NSX) * kXSlot + (wt * (BT / NWT) + 32 * j + m32) * 128 +
+                                            16 * ((4 * h + kk) ^ ((m32 / 2) % 8)));
+        };
+        auto read_w = [&](int s, auto jc) {  // s % 8 == J: block 2 (J % kSpW) + h of the wave's rows
+            constexpr int J = decltype(jc)::value % 8, O = J & 1;
+            const char* wt_base = wring + ((s / kSpW) % NSW) * kWSlot + wr * (BR / NWR) * kWRow + m32 * kWRow +
+                                  16 * ((2 * (J % kSpW) + h) ^ ((m32 / (16 / kWC)) % kWC));
+            const char* sc = sring + ((s >> 3) & 1) * kSSlot + 2 * J + h + 16 * (wr * (BR / NWR) + m32);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                C[O][i] = *(const u32x4*)(wt_base + 32 * kWRow * i);
+                f[O][i] = mx4_scale(*(const uint8_t*)(sc + 512 * i));
+            }
+        };
+        // Step kk's products; between them the reads of the next step (sn, nc)'s tokens and stage
+        // s's share of copies, as in k_mx4_gemm4: stage s sends out the tokens of stage
+        // s + NSX - 1 and before them, in a slot's first stage, the codes NSW - 1 slots on and,
+        // in a period's first, the next period's scales.
+        auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
+            constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
+            constexpr int kS = J == 0 ? kSInst : 0, kW = J % kSpW == 0 ? kWInst : 0;
+            constexpr int kTot = kS + kW + kXInst, M = 4 * MI * NJ;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const u32x4 A =
+                    widen_mx4(kk == 0 ? C[O][i].x : kk == 1 ? C[O][i].y : kk == 2 ? C[O][i].z : C[O][i].w, f[O][i]);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const int ql = i * NJ + j, q = kk * MI * NJ + ql;  // this product of the step, of the stage
+#pragma unroll
+                    for (int r = 0; r < NJ; ++r)
+                        if (r * MI == ql) read_x(sn, nc, r);
+#pragma unroll
+                    for (int c = 0; c < kTot; ++c) {
+                        if (c * M / kTot != q) continue;
+                        if (c < kS) copy_s(s / 8 + 1, c < kS ? c : 0);
+                        else if (c < kS + kW) copy_w(s / kSpW + NSW - 1, c < kS + kW ? c - kS : 0);
+                        else copy_x(s + NSX - 1, c - kS - kW);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, Bv[kk & 1][j]), __builtin_bit_cast(bf16x8, A), acc[i][j], 0, 0, 0);
+                    if (j + 1 < NJ) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
+        using C2 = std::integral_constant<int, 2>;
+        using C3 = std::integral_constant<int, 3>;
+        auto stage = [&](int s, auto jc) {  // s % 8 == J
+            constexpr int J = decltype(jc)::value;
+            products(s, C0(), jc, s, C1());
+            products(s, C1(), jc, s, C2());
+            products(s, C2(), jc, s, C3());
+            // in flight beyond what stage s + 1 needs: this stage's copies so far and those of the
+            // NSX - 3 stages before it (its codes and scales went out no later than its tokens)
+            constexpr auto pending = [] {
+                int n = 0;
+                for (int d = 0; d <= NSX - 3; ++d) {
+                    const int j = (J - d + 8) % 8, M = 4 * MI * NJ;
+                    const int kTot = (j == 0 ? kSInst : 0) + (j % kSpW == 0 ? kWInst : 0) + kXInst;
+                    int sent = kTot;
+                    if (d == 0) {  // the last step's copies are still to come
+                        sent = 0;
+                        for (int c = 0; c < kTot; ++c) sent += c * M / kTot < M - MI * NJ ? 1 : 0;
+                    }
+                    n += sent;
+                }
+                return n;
+            }();
+            wait_vmcnt_lgkm<pending>();
+            __builtin_amdgcn_s_barrier();
+            read_w(s + 1, std::integral_constant<int, J + 1>());
+            products(s, C3(), jc, s + 1, C0());
+        };
+        wait_vmcnt<(NSX - 2) * kXInst>();
+        __builtin_amdgcn_s_barrier();
+        read_w(0, C0());
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) read_x(0, C0(), j);
+        for (int s = 0; s < nk; s += 8) {  // (uniform branches)
+            stage(s, std::integral_constant<int, 0>());
+            if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>());
+            if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>());
+            if (s + 3 < nk) stage(s + 3, std::integral_constant<int, 3>());
+            if (s + 4 < nk) stage(s + 4, std::integral_constant<int, 4>());
+            if (s + 5 < nk) stage(s + 5, std::integral_constant<int, 5>());
+            if (s + 6 < nk) stage(s + 6, std::integral_constant<int, 6>());
+            if (s + 7 < nk) stage(s + 7, std::integral_constant<int, 7>());
+        }
     }
     wait_vmcnt<0>();  // the empty copies past the end have landed
     store_tile<MI, NJ>(acc, y, N, T, r0 + wr * (BR / NWR), t0 + wt * (BT / NWT), m32, h);
@@ -852,14 +950,14 @@ hipError_t launch_gemm4(const Mx4Launch& l) {
     return hipGetLastError();
 }
 
-template <int BR, int BT, int WC, int NSX, int NSW, int NWR, int NWT>
+template <int BR, int BT, int WC, int NSX, int NSW, int NWR, int NWT, bool WHOLE>
 hipError_t launch_gemm16(const Mx4Launch& l) {
     int rt = 0;
     const GemmMats gm = gemm_mats(l.mats, l.wscales, l.n, BR, l.parts, &rt);
     const int ntt = (int)((l.T + BT - 1) / BT), GR = row_group(ntt);
     const unsigned blocks = tile_grid(rt, ntt, l.S);
     constexpr int lds = NSX * BT * 128 + NSW * BR * (WC / 2) + 2 * BR * 16;
-    k_mx4_gemm16<BR, BT, WC, NSX, NSW, NWR, NWT><<<dim3(blocks), dim3(64 * NWR * NWT), lds, l.s>>>(
+    k_mx4_gemm16<BR, BT, WC, NSX, NSW, NWR, NWT, WHOLE><<<dim3(blocks), dim3(64 * NWR * NWT), lds, l.s>>>(
         (const uint16_t*)l.x, gm, (int)l.T, (int)l.d_in, ntt, l.S, (int)l.kps, GR);
     return hipGetLastError();
 }
@@ -994,11 +1092,11 @@ hipError_t launch_mx4_product(const void* x, const uint8_t* xscales, int64_t T, 
         }
     } else {
         switch (pl.tile) {
-            case k256x256: e = launch_gemm16<256, 256, 128, 3, 3, 4, 2>(l); break;
-            case k128x128: e = launch_gemm16<128, 128, 128, 3, 2, 2, 2>(l); break;
-            case k128x64: e = launch_gemm16<128, 64, 256, 4, 2, 2, 2>(l); break;
-            case k128x32: e = launch_gemm16<128, 32, 256, 4, 2, 4, 1>(l); break;
-            default: e = launch_gemm16<64, 32, 256, 4, 2, 2, 1>(l); break;
+            case k256x256: e = launch_gemm16<256, 256, 128, 3, 3, 4, 2, false>(l); break;
+            case k128x128: e = launch_gemm16<128, 128, 128, 3, 2, 2, 2, false>(l); break;
+            case k128x64: e = launch_gemm16<128, 64, 256, 4, 2, 2, 2, true>(l); break;
+            case k128x32: e = launch_gemm16<128, 32, 256, 4, 2, 4, 1, true>(l); break;
+            default: e = launch_gemm16<64, 32, 256, 4, 2, 2, 1, true>(l); break;
         }
     }
     if (e != hipSuccess || pl.S == 1) return e;
