@@ -34,14 +34,13 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
 // suser[p] = user of sorted position p (p < meta[2]).
 //
 // Sorting by counting: a token's place among the (user, token) keys is the number of keys
-// below its own.  A block takes 16 tokens, 16 lanes each share the count of one; block 0
-// also counts the valid tokens and writes the status (k_tile_plan then makes the items).  One
-// block's bitonic sort, with its barriers, took 14 us at 512 tokens and 34 us at 1144; this
-// takes 3 us at both.
+// below its own.  A block takes 4 tokens, the 64 lanes of a wave share the count of one; block 0
+// also counts the valid tokens and writes the status (k_tile_plan then makes the items).  It
+// takes 4.7 us at 512 tokens and 5.2 us at 1144 (8.2 with 16 lanes to a token).
 __global__ void __launch_bounds__(256)
 k_group(const int32_t* __restrict__ ids, int T, int U, int32_t* __restrict__ perm,
         int32_t* __restrict__ suser, uint32_t* __restrict__ meta) {
-    const int tid = threadIdx.x, i = (int)blockIdx.x * 16 + (tid >> 4), sl = tid & 15;
+    const int tid = threadIdx.x, i = (int)blockIdx.x * 4 + (tid >> 6), sl = tid & 63;
     auto user_of = [&](int j) {  // invalid users sort last
         const int u = ids[j];
         return u >= 0 && u < U ? u : U;
@@ -49,12 +48,12 @@ k_group(const int32_t* __restrict__ ids, int T, int U, int32_t* __restrict__ per
     const int ui = i < T ? user_of(i) : 0;
     int rank = 0;
 #pragma unroll 8
-    for (int j = sl; j < T; j += 16) {
+    for (int j = sl; j < T; j += 64) {
         const int uj = user_of(j);
         rank += (uj < ui || (uj == ui && j < i)) ? 1 : 0;
     }
 #pragma unroll
-    for (int off = 1; off < 16; off <<= 1) rank += __shfl_xor(rank, off);
+    for (int off = 1; off < 64; off <<= 1) rank += __shfl_xor(rank, off);
     if (sl == 0 && i < T && ui < U) {
         perm[rank] = i;
         suser[rank] = ui;
@@ -480,7 +479,7 @@ hipError_t launch_batch_prepare(const BatchPlan& pl, const void* x, const int32_
                            (int32_t*)(batch + pl.off_perm), (int32_t*)(batch + pl.off_user),
                            (int4*)(batch + pl.off_items), meta);
     } else {
-        hipLaunchKernelGGL(k_group, dim3((unsigned)((pl.T + 15) / 16)), dim3(256), 0, s, ids, (int)pl.T,
+        hipLaunchKernelGGL(k_group, dim3((unsigned)((pl.T + 3) / 4)), dim3(256), 0, s, ids, (int)pl.T,
                            pl.U, (int32_t*)(batch + pl.off_perm), (int32_t*)(batch + pl.off_user), meta);
     }
     err = hipGetLastError();
