@@ -472,7 +472,7 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
     // first stage before them the scales of the next period, spread evenly over its products.
     // (All at once, copies or reads hold up every wave's products while the address unit or
     // the LDS takes them in turn: 256 columns of a 256 x 256 block took 3600 cycles with the
-    // copies behind the barrier, 3250 with the reads alone in bursts.)
+    // copies behind the barrier, 3250 with the reads alone in bursts, and take 2820 like this.)
     auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
         constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
         constexpr int kS = J == 0 ? kSInst : 0, kTot = kS + kD, M = kSteps * MI * NJ;
@@ -994,13 +994,14 @@ k_mx4_reduce(const GemmMats gm, int T, int S) {
     }
 }
 
-// Tile and K split by a model of their time (us), fitted to 1100 measurements of all tiles
+// Tile and K split by a model of their time (us), fitted to 3700 measurements of the tiles
 // and splits at 17..8192 tokens on 700 x 1088 to 34816 x 5120 (graph replays on one MI355X):
 //   a + max(ceil(blocks / (256 occ)) b, ceil(blocks / 256) c) n + (S > 1: 2 + bytes / 3.5 TB/s)
 // with n the 256-column steps of a block's K part, occ the blocks a CU holds, a the fixed
-// cost, b one block's time per step, c a CU's per block and step.  The choice is within 2%
-// of the best measured on average (the worst 32%); the largest tile alone would be 60% off,
-// the smallest 75%.
+// cost, b one block's time per step, c a CU's per block and step.  The choice is 1.7%
+// (MX4 tokens) and 2.5% (bf16) off the best measured on average, 17% and 32% at the worst;
+// always the largest tile, with its best split, would be 54% and 72% off on average, always
+// the smallest 19% and 22%.
 struct TileCost {
     int tile, br, bt, occ;
     double a, b, c;
