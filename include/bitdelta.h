@@ -378,7 +378,8 @@ typedef enum { BD_MX4_TOKENS_BF16 = 0, BD_MX4_TOKENS_MX4 = 1 } bd_mx4_tokens;
 /* bd_apply with the base weight given as MX4 rows:
  *     y[t] = base(X[t]) + scale_u (.) (X[t] . S_u^T),
  * base as bd_base_gemm_mx4_n or bd_base_gemm_mx4x4_n (`tokens`).  bf16 X only
- * (BD_ERR_UNSUPPORTED for fp32), up to 8192 tokens, any scale mode.
+ * (BD_ERR_UNSUPPORTED for fp32), up to 8192 tokens, any scale mode.  Decode batches (1..16
+ * tokens, MATRIX or ROW scales, d_in <= 4096, bf16 tokens) take one launch.
  * workspace: >= bd_apply_mx4_workspace_bytes(...) bytes; other arguments, the status word
  * and errors as for bd_apply. */
 size_t bd_apply_mx4_workspace_bytes(const bd_compress_params* p, int64_t T, int32_t n_users,

@@ -537,25 +537,39 @@ bd_status bd_base_gemm_mx4x4_n(const uint8_t* x_codes, const uint8_t* x_scales, 
                          workspace, ws_bytes, stream);
 }
 
-// The workspace of bd_apply_mx4: the apply plan's | the quantised tokens | the base
-// product's.
+// The workspace of bd_apply_mx4: the apply plan's | the fp32 base product (decode batches
+// with bf16 y) | the quantised tokens | the base product's.
+//  fused: decode batches of bf16 tokens, MATRIX or ROW scales, rows of up to 4096 columns: one
+//         launch (k_decode_unit on MX4 rows).
+//  decode: the other batches of at most 16 tokens but GROUP scales, up to kMx4DecodeRows
+//         rows: the base product with the decode path's two launches around it.  16 tokens
+//         of 16 users, d_in 4096, microseconds against the prepared batch: 4096 rows 30 to
+//         42, 12288 52 to 58, 16384 62 to 60, 28672 102 to 89; 2 tokens of one user at
+//         d_in 8192: 23 to 38, 42 to 45, 48 to 45, 77 to 57 (every 16 rows read all encoded
+//         tokens again, which the prepared batch's blocks of 256 rows do not).
+//  otherwise the prepared batch.
+constexpr int64_t kMx4DecodeRows = 12288;
 struct Mx4ApplyPlan {
     ApplyPlan a;
-    bool x4 = false, dec = false;  // dec: the one-launch decode path
-    size_t off_xc = 0, off_xs = 0, off_base = 0, total = 0;
+    bool x4 = false, fused = false, decode = false;
+    size_t off_yb = 0, off_xc = 0, off_xs = 0, off_base = 0, total = 0;
 };
 static bd_status make_mx4_plan(const bd_compress_params* p, int64_t T, int32_t n_users,
                                int64_t d_out, int64_t d_in, bd_dtype x_dtype, bd_dtype y_dtype,
                                bd_mx4_tokens tokens, Mx4ApplyPlan* pl) {
     if (!p || (tokens != BD_MX4_TOKENS_BF16 && tokens != BD_MX4_TOKENS_MX4)) return BD_ERR_INVALID_ARG;
     pl->x4 = tokens == BD_MX4_TOKENS_MX4;
-    pl->dec = !pl->x4 && q8_path_supported(x_dtype, T, p->mode, d_in);
-    bd_status st = make_apply_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, &pl->a, pl->dec);
+    pl->fused = !pl->x4 && q8_path_supported(x_dtype, T, p->mode, d_in);
+    pl->decode = !pl->fused && d_out <= kMx4DecodeRows && decode_path_supported(x_dtype, T, p->mode);
+    bd_status st = make_apply_plan(p, T, n_users, d_out, d_in, x_dtype, y_dtype, &pl->a,
+                                   pl->fused || pl->decode);
     if (st != BD_OK) return st;
     if (x_dtype != BD_BF16 || !mx4_product_supported(pl->x4, T, d_in, d_out)) return BD_ERR_UNSUPPORTED;
     size_t off = align_up(pl->a.total);
     pl->total = off;
-    if (pl->dec) return BD_OK;
+    if (pl->fused) return BD_OK;
+    pl->off_yb = off;
+    if (pl->decode && y_dtype == BD_BF16) off += align_up((size_t)T * d_out * 4);
     pl->off_xc = off;
     if (pl->x4) off += align_up((size_t)T * d_in / 2);
     pl->off_xs = off;
@@ -595,20 +609,25 @@ bd_status bd_apply_mx4(const void* x, bd_dtype x_dtype, int64_t T, int64_t d_in,
             (scales_bank && !aligned(scales_bank, 16)))
             return BD_ERR_INVALID_ARG;
     }
-    if (pl.dec) {
+    if (pl.fused) {
         e = launch_decode_mx4(T, n_users, d_in, pl.a.delta, x, user_ids, w_codes, w_scales,
                               signs_bank, scales_bank, y, y_dtype, ws, s);
         return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
     }
-    e = launch_batch_prepare(pl.a.batch, x, user_ids, ws, s);
+    e = pl.decode ? launch_decode_prep(pl.a.dec, n_users, pl.a.delta, x, user_ids, scales_bank, ws, s)
+                  : launch_batch_prepare(pl.a.batch, x, user_ids, ws, s);
     if (e != hipSuccess || T == 0) return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
-    float* yacc = y_dtype == BD_F32 ? (float*)y : (float*)(ws + pl.a.off_yf);
+    float* yacc = y_dtype == BD_F32 ? (float*)y : (float*)(ws + (pl.decode ? pl.off_yb : pl.a.off_yf));
     const GemmMatArg m = {w_codes, yacc, d_out};
     uint8_t *xc = (uint8_t*)(ws + pl.off_xc), *xs = (uint8_t*)(ws + pl.off_xs);
     if (pl.x4) e = launch_mx4_quantize(x, BD_BF16, T, d_in, xc, xs, nullptr, s);
     if (e == hipSuccess)
         e = launch_mx4_product(pl.x4 ? (const void*)xc : x, pl.x4 ? xs : nullptr, T, d_in, &m,
                                &w_scales, 1, pl.total > pl.off_base ? ws + pl.off_base : nullptr, s);
+    if (e == hipSuccess && pl.decode) {
+        e = launch_decode_given(pl.a.dec, pl.a.delta, x, yacc, signs_bank, scales_bank, y, y_dtype, ws, s);
+        return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
+    }
     if (e == hipSuccess)
         e = launch_delta(pl.a.batch, pl.a.delta, ws, x, signs_bank, scales_bank, yacc, s);
     if (e == hipSuccess && y_dtype == BD_BF16)

@@ -28,7 +28,9 @@
 //                  other tokens enter with block scale 2^-127 (E8M0 code 0),
 //                  so one accumulator collects every user's product in its own
 //                  token columns.  Partial tiles are summed in LDS in wave order
-//                  and written once: no atomics, no read-modify-write of y.
+//                  and written once: no atomics, no read-modify-write of y.  On an
+//                  MX4 base the base product is computed before, by its own kernels,
+//                  and all waves take the delta (GIVEN).
 //
 // Sign bits to fp4: nibble = 0x2 | (bit << 3), i.e. +1.0 for a negative delta
 // and -1.0 for a non-negative one, so the accumulator holds -(X S^T) and the
@@ -239,15 +241,18 @@ struct Unit {
     uint32_t e;
 };
 
-template <int MODE>
+// GIVEN: the base product is already in yb [T][d_out] (fp32; may be y itself), all waves
+// take the delta products.
+template <int MODE, bool GIVEN>
 __global__ void __launch_bounds__(64 * kDecodeWaves)
 k_decode(const uint16_t* __restrict__ x, int T, int64_t d_in, int64_t dpad,
-         const uint16_t* __restrict__ w, int64_t d_out, const uint64_t* __restrict__ signs,
+         const uint16_t* __restrict__ w, const float* yb, int64_t d_out,
+         const uint64_t* __restrict__ signs,
          uint64_t sstride, const void* __restrict__ scales, int sdtype, int64_t per_user,
          const uint32_t* __restrict__ meta, const int32_t* __restrict__ perm,
          const int32_t* __restrict__ suser, const int4* __restrict__ seg,
          const uint16_t* __restrict__ xs, const uint8_t* __restrict__ x8,
-         const uint8_t* __restrict__ e8, void* __restrict__ y, int ydtype) {
+         const uint8_t* __restrict__ e8, void* y, int ydtype) {
     __shared__ f32x4 red_base[kDecodeWaves][64];   // per K slice of the base product
     __shared__ f32x4 red_delta[kDecodeWaves][64];  // per delta wave
     const int lane = threadIdx.x & 63;
@@ -255,8 +260,8 @@ k_decode(const uint16_t* __restrict__ x, int T, int64_t d_in, int64_t dpad,
     const int m = lane & 15, g = lane >> 4;
     const int nseg = (int)meta[1], nv = (int)meta[2];
     // waves split by HBM bytes per row: 2 d_in (base) against nseg d_in / 8 (delta)
-    int nwb = kDecodeWaves;
-    if (nseg > 0) {
+    int nwb = GIVEN ? 0 : kDecodeWaves;
+    if (!GIVEN && nseg > 0) {
         nwb = (16 * kDecodeWaves + (16 + nseg) / 2) / (16 + nseg);
         nwb = nwb < 1 ? 1 : (nwb > kDecodeWaves - 1 ? kDecodeWaves - 1 : nwb);
     }
@@ -264,7 +269,7 @@ k_decode(const uint16_t* __restrict__ x, int T, int64_t d_in, int64_t dpad,
     const int64_t rowA = r0 + m < d_out ? r0 + m : d_out - 1;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 
-    if (wv < nwb) {
+    if (!GIVEN && wv < nwb) {
         // ---- base: the K steps of 32 columns form kDecodeWaves fixed slices (slice s =
         // steps s, s + kDecodeWaves, ...), each summed in step order and stored to LDS;
         // wave wv takes slices wv, wv + nwb, ...  The partition, and so the rounding, does
@@ -422,10 +427,16 @@ k_decode(const uint16_t* __restrict__ x, int T, int64_t d_in, int64_t dpad,
 
     // ---- epilogue: base slices + factor * delta partials, each in a fixed order
     f32x4 vb = {0.f, 0.f, 0.f, 0.f}, vd = {0.f, 0.f, 0.f, 0.f};
-    for (int q = 0; q < kDecodeWaves; ++q) vb += red_base[q][lane];
+    if constexpr (!GIVEN)
+        for (int q = 0; q < kDecodeWaves; ++q) vb += red_base[q][lane];
     for (int q = 0; q < kDecodeWaves - nwb; ++q) vd += red_delta[q][lane];
     if (m >= T) return;
     const int64_t o = r0 + 4 * g;
+    if constexpr (GIVEN) {
+        const float* src = yb + (int64_t)perm[m] * d_out + o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vb[e] = o + e < d_out ? src[e] : 0.f;
+    }
     float f[4] = {0.f, 0.f, 0.f, 0.f};
     if (m < nv) {
         const int64_t u = suser[m];
@@ -1276,13 +1287,16 @@ hipError_t launch_decode_prep(const DecodePlan& pl, int U, const DeltaPlan& dp, 
     return hipGetLastError();
 }
 
-hipError_t launch_decode_main(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
-                              const void* wb, const uint64_t* signs, const void* scales, void* y,
-                              int ydtype, const char* ws, hipStream_t s) {
+template <bool GIVEN>
+static hipError_t launch_decode_any(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
+                                    const void* wb, const float* yb, const uint64_t* signs,
+                                    const void* scales, void* y, int ydtype, const char* ws,
+                                    hipStream_t s) {
     const dim3 grid((unsigned)((dp.d_out + 15) / 16));
 #define BD_DECODE(MODE)                                                                           \
-    hipLaunchKernelGGL(k_decode<MODE>, grid, dim3(64 * kDecodeWaves), 0, s, (const uint16_t*)x,   \
-                       (int)pl.T, pl.d_in, pl.dpad, (const uint16_t*)wb, dp.d_out, signs,          \
+    hipLaunchKernelGGL((k_decode<MODE, GIVEN>), grid, dim3(64 * kDecodeWaves), 0, s,              \
+                       (const uint16_t*)x, (int)pl.T, pl.d_in, pl.dpad, (const uint16_t*)wb, yb,   \
+                       dp.d_out, signs,                                                            \
                        sign_stride(dp.sstride, dp.d_out, pl.d_in), scales, dp.sdtype,              \
                        scale_stride(dp), (const uint32_t*)(ws + pl.off_meta),                      \
                        (const int32_t*)(ws + pl.off_perm), (const int32_t*)(ws + pl.off_suser),    \
@@ -1296,6 +1310,18 @@ hipError_t launch_decode_main(const DecodePlan& pl, const DeltaPlan& dp, const v
     }
 #undef BD_DECODE
     return hipGetLastError();
+}
+
+hipError_t launch_decode_main(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
+                              const void* wb, const uint64_t* signs, const void* scales, void* y,
+                              int ydtype, const char* ws, hipStream_t s) {
+    return launch_decode_any<false>(pl, dp, x, wb, nullptr, signs, scales, y, ydtype, ws, s);
+}
+
+hipError_t launch_decode_given(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
+                               const float* yb, const uint64_t* signs, const void* scales, void* y,
+                               int ydtype, const char* ws, hipStream_t s) {
+    return launch_decode_any<true>(pl, dp, x, nullptr, yb, signs, scales, y, ydtype, ws, s);
 }
 
 bool fused_path_supported(int xdtype, int64_t T, int mode, int64_t d_in) {

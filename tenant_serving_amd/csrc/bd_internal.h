@@ -243,6 +243,11 @@ hipError_t launch_decode_prep(const DecodePlan& pl, int U, const DeltaPlan& dp, 
 hipError_t launch_decode_main(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
                               const void* wb, const uint64_t* signs, const void* scales, void* y,
                               int ydtype, const char* ws, hipStream_t s);
+// The delta half of launch_decode_main onto a base product yb [T][d_out] (fp32; y itself
+// for fp32 outputs).
+hipError_t launch_decode_given(const DecodePlan& pl, const DeltaPlan& dp, const void* x,
+                               const float* yb, const uint64_t* signs, const void* scales, void* y,
+                               int ydtype, const char* ws, hipStream_t s);
 bool fused_path_supported(int xdtype, int64_t T, int mode, int64_t d_in);
 // Writes the status word at ws (bad user ids) and y; reads nothing else of ws.
 hipError_t launch_decode_fused(int64_t T, int U, int64_t d_in, const DeltaPlan& dp, const void* x,

@@ -259,6 +259,8 @@ APPLY = [
     ("group", B.BD_F32, 136, 2048, seeded_ids(4, 70, 5), 5, torch.float32),
     ("group", B.BD_F32, 136, 1024, seeded_ids(5, 9, 5), 5, torch.bfloat16),
     ("matrix", B.BD_F32, 300, 576, seeded_ids(6, 260, 7), 7, torch.bfloat16),
+    ("col", B.BD_F32, 12288, 192, seeded_ids(7, 6, 3), 3, torch.bfloat16),
+    ("col", B.BD_F32, 12291, 192, seeded_ids(7, 6, 3), 3, torch.float32),
 ]
 
 
