@@ -895,8 +895,10 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
 }
 
 bool mx4_product_supported(bool x4, int64_t T, int64_t d_in, int64_t d_out) {
-    return d_in % 64 == 0 && T * d_in * (x4 ? 1 : 4) < ((int64_t)1 << 32) &&
-           d_out * d_in < ((int64_t)1 << 32) && d_out < ((int64_t)1 << 30) && T < ((int64_t)1 << 20);
+    // (each size first: their products then stay inside 64 bits)
+    return d_in % 64 == 0 && d_in < ((int64_t)1 << 30) && d_out < ((int64_t)1 << 30) &&
+           T < ((int64_t)1 << 20) && T * d_in * (x4 ? 1 : 4) < ((int64_t)1 << 32) &&
+           d_out * d_in < ((int64_t)1 << 32);
 }
 
 namespace {

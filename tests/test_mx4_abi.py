@@ -73,6 +73,9 @@ def test_product_refusals():
         assert f(d=0) == B.BD_ERR_SHAPE
         assert f(d_in=1 << 20, d=1 << 13) == B.BD_ERR_UNSUPPORTED  # 32-bit offsets
         assert f(T=1 << 19, d_in=1 << 14) == B.BD_ERR_UNSUPPORTED
+        assert f(d_in=1 << 62, d=4) == B.BD_ERR_UNSUPPORTED  # sizes whose product wraps to 0
+        assert f(T=1 << 58) == B.BD_ERR_UNSUPPORTED
+        assert f(d=1 << 58) == B.BD_ERR_UNSUPPORTED
         assert f(x=None) == B.BD_ERR_INVALID_ARG
         assert f(x=A + 8) == B.BD_ERR_INVALID_ARG
         assert f(w=None) == B.BD_ERR_INVALID_ARG
