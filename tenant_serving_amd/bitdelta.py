@@ -801,9 +801,20 @@ def bd_apply_mx4(x, codes, scales, signs_bank, scales_bank, p, n_users, user_ids
                       user_ids, y, workspace, _tokens(tokens), stream)
 
 
+def _current(stream, t):
+    """The context of a helper's call on `stream` (a stream or its handle): what the call
+    allocates on t's device is that stream's, as under torch.cuda.stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=t.device)
+    return torch.cuda.stream(stream)
+
+
 def quantize_mx4(w: torch.Tensor, values: bool = False, stream=None):
     """(codes, scales) of w in MX4, and with `values` also what they stand for, in w's
     dtype (bd_quantize_mx4)."""
+    if stream is not None:
+        with _current(stream, w):
+            return quantize_mx4(w, values)
     idx, rows, cols = _tokens_2d(w, "w", (torch.float32, torch.bfloat16))
     codes = w.new_empty((rows, cols // 2), dtype=torch.uint8)
     scales = w.new_empty((rows, 16 * ((cols + 511) // 512)), dtype=torch.uint8)
@@ -814,13 +825,20 @@ def quantize_mx4(w: torch.Tensor, values: bool = False, stream=None):
 
 def dequantize_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bfloat16,
                    stream=None) -> torch.Tensor:
-    out = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=out_dtype, device=codes.device)
-    _check(bd_dequantize_mx4(codes, scales, out, stream), "bd_dequantize_mx4")
+    _, rows, cols = _mx4(codes, scales, "base")
+    if stream is not None:
+        with _current(stream, codes):
+            return dequantize_mx4(codes, scales, out_dtype)
+    out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device)
+    _check(bd_dequantize_mx4(codes, scales, out), "bd_dequantize_mx4")
     return out
 
 
 def base_gemm_mx4(x: torch.Tensor, bases, ws=None, stream=None):
     """[x . W^T] in fp32 for 1..4 MX4 matrices (codes, scales) and bf16 tokens x."""
+    if stream is not None:
+        with _current(stream, x):
+            return base_gemm_mx4(x, bases, ws)
     idx, T, d_in = _tokens_2d(x, "x", (torch.bfloat16,))
     rows = _mx4_bases(bases, idx, d_in)
     ys = [x.new_empty((T, n), dtype=torch.float32) for n in rows]
@@ -837,6 +855,9 @@ def base_gemm_mx4(x: torch.Tensor, bases, ws=None, stream=None):
 def base_gemm_mx4x4(xq, bases, ws=None, stream=None):
     """base_gemm_mx4 on MX4 tokens xq = (codes, scales)."""
     x_codes, x_scales = xq
+    if stream is not None:
+        with _current(stream, x_codes):
+            return base_gemm_mx4x4(xq, bases, ws)
     idx, T, d_in = _mx4(x_codes, x_scales, "token")
     rows = _mx4_bases(bases, idx, d_in)
     ys = [x_codes.new_empty((T, n), dtype=torch.float32) for n in rows]
@@ -854,6 +875,10 @@ def apply_mx4(x, codes, scales, signs_bank, scales_bank, p, user_ids, y_dtype=to
               tokens="bf16", ws=None, stream=None, check: bool = False) -> torch.Tensor:
     """bd_apply on an MX4 base (codes, scales); tokens: how the base product reads x,
     "bf16" as it is or "mx4" quantised within the call."""
+    if stream is not None:
+        with _current(stream, x):
+            return apply_mx4(x, codes, scales, signs_bank, scales_bank, p, user_ids, y_dtype, tokens,
+                             ws, None, check)
     U, tok = signs_bank.shape[0], _tokens(tokens)
     idx, T, d_in, d_out = _apply_mx4_checks(x, codes, scales, signs_bank, scales_bank, p, U, user_ids)
     y = x.new_empty((T, d_out), dtype=y_dtype)

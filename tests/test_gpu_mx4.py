@@ -170,7 +170,9 @@ def test_products_match_oracle(T, d_outs, d_in, x4):
 
 
 TILE_CASES = [((14336,), 512, 512), ((4100, 300), 1088, 1000), ((700,), 1536, 333), ((4096,), 4096, 129),
-              ((1024, 1024, 4096), 2048, 257), ((5120,), 8192, 70), ((160,), 64, 2100)]
+              ((1024, 1024, 4096), 2048, 257), ((5120,), 8192, 70), ((160,), 64, 2100),
+              ((2050,), 1088, 1000), ((2050,), 1088, 3000), ((5123,), 448, 2060), ((2050,), 2112, 4100),
+              ((700,), 8256, 333), ((1000,), 8256, 257), ((2050,), 8256, 520), ((2050,), 8256, 1000)]
 
 
 @pytest.mark.parametrize("x4", [False, True], ids=["bf16", "mx4"])
@@ -233,6 +235,43 @@ def test_products_captured_and_on_another_stream(x4):
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("as_int", [False, True], ids=["stream", "handle"])
+def test_helpers_on_a_given_stream(as_int):
+    """What a helper allocates for a call on another stream is that stream's: blocks that
+    the current stream has freed with work on them still to run are not handed to it."""
+    T, n, d_in = 80, 96, 4096
+    base, _ = base_of(n, d_in)
+    x = tokens_of(T, d_in, seed=3)[0].to(DEV)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_int else side
+    calls = [lambda s: B.base_gemm_mx4(x, [base], stream=s)[0],
+             lambda s: B.base_gemm_mx4x4(B.quantize_mx4(x, stream=s), [base], stream=s)[0],
+             lambda s: B.dequantize_mx4(*base, torch.float32, stream=s)]
+    p = B.params("matrix")
+    signs = torch.randint(-2 ** 62, 2 ** 62, (2, n, d_in // 64), device=DEV)
+    sc = torch.rand(2, 1, device=DEV)
+    ids = (torch.arange(T, device=DEV) % 2).int()
+    calls += [lambda s: B.apply_mx4(x, *base, signs, sc, p, ids, stream=s, check=True),
+              lambda s: B.apply_mx4(x, *base, signs, sc, p, ids, tokens="mx4", stream=s)]
+    want = [f(None) for f in calls]
+    for f, w in zip(calls, want):  # the default stream's handle is 0
+        assert torch.equal(f(torch.cuda.default_stream().cuda_stream), w)
+    big = torch.ones(8192, 8192, device=DEV)
+    for f, w in zip(calls, want):
+        torch.cuda.synchronize()
+        for _ in range(4):
+            big @ big  # the current stream is busy ...
+        junk = [torch.empty(m, dtype=torch.uint8, device=DEV) for m in [T * n * 4, n * d_in * 4] * 4 + [1 << 23] * 2]
+        for j in junk:
+            j.fill_(0xFF)
+        del junk, j  # ... and these blocks, free for its next tensors, are still to be filled
+        got = f(stream)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, w)
+        del got
+
+
 def test_empty_batch():
     base = base_of(40, 128)[0]
     x = torch.empty(0, 128, dtype=torch.bfloat16, device=DEV)
@@ -261,6 +300,11 @@ APPLY = [
     ("matrix", B.BD_F32, 300, 576, seeded_ids(6, 260, 7), 7, torch.bfloat16),
     ("col", B.BD_F32, 12288, 192, seeded_ids(7, 6, 3), 3, torch.bfloat16),
     ("col", B.BD_F32, 12291, 192, seeded_ids(7, 6, 3), 3, torch.float32),
+    ("matrix", B.BD_F32, 80, 128, np.full(64, 1, np.int32), 2, torch.float32),
+    ("row", B.BD_F32, 80, 128, np.full(65, 1, np.int32), 2, torch.bfloat16),
+    ("matrix", B.BD_F32, 80, 128, seeded_ids(8, 1025, 40), 40, torch.float32),
+    ("row", B.BD_F32, 48, 64, seeded_ids(9, 8192, 300), 300, torch.float32),
+    ("matrix", B.BD_F32, 48, 64, np.full(8192, -1, np.int32), 1, torch.float32),
 ]
 
 
