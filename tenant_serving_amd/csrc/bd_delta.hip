@@ -97,14 +97,14 @@ __device__ __forceinline__ int block_scan(int v, int32_t* sc, int* total) {
     __syncthreads();  // (sc's readers of an earlier scan)
     if (l == 63) sc[w] = incl;
     __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll 1
-    for (int q = 0; q < NW; ++q) {
-        const int o = sc[q];
-        if (q < w) before = MAX ? (before > o ? before : o) : before + o;
-        all = MAX ? (all > o ? all : o) : all + o;
+    int sw = l < NW ? sc[l] : 0;  // every wave scans the NW words itself
+#pragma unroll
+    for (int off = 1; off < NW; off <<= 1) {
+        const int o = __shfl_up(sw, off);
+        if (l >= off) sw = MAX ? (sw > o ? sw : o) : sw + o;
     }
-    if (total) *total = all;
+    const int prev = __shfl(sw, w > 0 ? w - 1 : 0), before = w > 0 ? prev : 0;
+    if (total) *total = __shfl(sw, NW - 1);
     int excl = __shfl_up(incl, 1);
     if (l == 0) excl = 0;
     return MAX ? (before > excl ? before : excl) : before + excl;
@@ -112,8 +112,7 @@ __device__ __forceinline__ int block_scan(int v, int32_t* sc, int* total) {
 
 // ITEMS: the block (kPlanThreads threads) first cuts the sorted users into the work items;
 // otherwise one wave takes them from k_group_wave.  One block's latencies in turn bound it:
-// 11.2 us at 512 tokens, 14.1 us at 1144.  The loops stay rolled and work on LDS: each
-// instruction runs a few times, on one CU, and has to be fetched first.
+// 8.5 us at 512 tokens, 11.7 us at 1144 (11.4 and 14.6 with LDS reads one after the other).
 template <bool ITEMS>
 __global__ void __launch_bounds__(ITEMS ? kPlanThreads : 64)
 k_tile_plan(int4* __restrict__ items, const int32_t* __restrict__ suser,
@@ -177,14 +176,12 @@ k_tile_plan(int4* __restrict__ items, const int32_t* __restrict__ suser,
     if (!ITEMS && tid == 0) ist[nit] = (uint16_t)nv;
     __syncthreads();
     for (int k = tid; k < nit; k += kThreads) {
-        const int c = ist[k + 1] - ist[k];
-        int cl = c > 16 ? c - 16 : c, j = k + 1;
-#pragma unroll 1
-        for (; j < nit; ++j) {
-            const int cj = ist[j + 1] - ist[j];
-            if (cl + cj > 16) break;
-            cl += cj;
-        }
+        const int p1 = ist[k + 1], c = p1 - ist[k];
+        const int end = p1 + 16 - (c > 16 ? c - 16 : c);  // where the open tile is full
+        int j = k + 1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // (an item has a position or more; ends grow with it)
+            j += k + 1 + i < nit && ist[k + 2 + i < kMaxT ? k + 2 + i : kMaxT] <= end ? 1 : 0;
         jump[0][k] = (uint16_t)j;
     }
     if (tid == 0) jump[0][nit] = jump[1][nit] = (uint16_t)nit;
@@ -228,9 +225,11 @@ k_tile_plan(int4* __restrict__ items, const int32_t* __restrict__ suser,
     // distinct users of each tile: user changes over its (sorted) positions
     for (int t = tid; t < nt; t += kThreads) {
         const int a = st[t], e = st[t + 1];
-        int cnt = 0;
-#pragma unroll 1
-        for (int q = a; q < e; ++q) cnt += q == a || su[q + 1] != su[q] ? 1 : 0;
+        int u[16], cnt = a < e ? 1 : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = su[a + i < e ? a + i + 1 : e];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) cnt += u[i] != u[i - 1] ? 1 : 0;
         snu[t] = (uint8_t)cnt;
     }
     __syncthreads();
@@ -239,7 +238,7 @@ k_tile_plan(int4* __restrict__ items, const int32_t* __restrict__ suser,
     for (int t = tid; t < nt; t += kThreads) {
         const int v = snu[t];
         int rank = 0, pre = 0;
-#pragma unroll 4
+#pragma unroll 16
         for (int q = 0; q < nt; ++q) {
             const int o = snu[q];
             const bool before = o > v || (o == v && q < t);

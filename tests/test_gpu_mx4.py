@@ -97,14 +97,20 @@ def test_non_finite_blocks(dtype):
     assert np.array_equal(values.double().cpu().numpy(), ov, equal_nan=True)
     assert np.array_equal(B.dequantize_mx4(codes, scales, dtype).double().cpu().numpy(), ov, equal_nan=True)
     # products: the rows (and tokens) that hold such a block are NaN, the others are not
-    x, xv = tokens_of(5, 576)
-    (y,) = B.base_gemm_mx4(x.to(DEV), [(codes, scales)])
     ok = np.array([0, 3, 5])
-    got = y.cpu().numpy()
-    assert np.isnan(got[:, [1, 2, 4]]).all()
-    assert_product(got[:, ok], xv, ov[ok])
-    (y4,) = B.base_gemm_mx4x4(B.quantize_mx4(x.to(DEV)), [(codes, scales)])
-    assert np.isnan(y4.cpu().numpy()[:, [1, 2, 4]]).all() and np.isfinite(y4.cpu().numpy()[:, ok]).all()
+    for T in (5, 80):
+        x, xv = tokens_of(T, 576)
+        (y,) = B.base_gemm_mx4(x.to(DEV), [(codes, scales)])
+        got = y.cpu().numpy()
+        assert np.isnan(got[:, [1, 2, 4]]).all()
+        assert_product(got[:, ok], xv, ov[ok])
+        (y4,) = B.base_gemm_mx4x4(B.quantize_mx4(x.to(DEV)), [(codes, scales)])
+        assert np.isnan(y4.cpu().numpy()[:, [1, 2, 4]]).all() and np.isfinite(y4.cpu().numpy()[:, ok]).all()
+        x[3, 575] = float("inf")  # a token's infinity stays that token's
+        for y in B.base_gemm_mx4(x.to(DEV), [(codes, scales)]) + \
+                B.base_gemm_mx4x4(B.quantize_mx4(x.to(DEV)), [(codes, scales)]):
+            fin = np.isfinite(y.cpu().numpy()[:, ok])
+            assert not fin[3].any() and np.delete(fin, 3, 0).all()
     clean = base_of(16, 576)[0]
     (y4t,) = B.base_gemm_mx4x4((codes, scales), [clean])  # the same rows as tokens
     bad = np.isnan(y4t.cpu().numpy())
