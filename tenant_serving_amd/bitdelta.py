@@ -805,7 +805,9 @@ def _current(stream, t):
     """The context of a helper's call on `stream` (a stream or its handle): what the call
     allocates on t's device is that stream's, as under torch.cuda.stream."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=t.device)
+        raw = int(getattr(stream, "cuda_stream", stream))
+        # (ExternalStream takes a handle of 0 for none and picks a stream from its pool)
+        stream = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
     return torch.cuda.stream(stream)
 
 
