@@ -722,10 +722,14 @@ def _mx4_outs(ys, T, rows, workspace, idx):
         _dev(workspace, "workspace", None, None, ys[0].device)
 
 
-def _mx4_args(bases, rows, ys, ws):
-    n = len(rows)
-    P, N = ctypes.c_void_p * n, ctypes.c_int64 * n
-    return (n, P(*[c.data_ptr() for c, _ in bases]), P(*[s.data_ptr() for _, s in bases]), N(*rows),
+# host arrays of 1..4 pointers and sizes (made once: their types cost as much as a call)
+_PTRS = [None] + [ctypes.c_void_p * n for n in range(1, 5)]
+_SIZES = [None] + [ctypes.c_int64 * n for n in range(1, 5)]
+
+
+def _mx4_args(bases, sizes, ys, ws):
+    P = _PTRS[len(ys)]
+    return (len(ys), P(*[c.data_ptr() for c, _ in bases]), P(*[s.data_ptr() for _, s in bases]), sizes,
             P(*[y.data_ptr() for y in ys]), None if ws is None else ws.data_ptr(),
             0 if ws is None else _nbytes(ws))
 
@@ -742,7 +746,7 @@ def bd_base_gemm_mx4_n(x, bases, ys, workspace=None, stream=None) -> int:
     rows = _mx4_bases(bases, idx, d_in)
     _mx4_outs(ys, T, rows, workspace, idx)
     return _run(lib().bd_base_gemm_mx4_n, idx, stream, x.data_ptr(), BD_BF16, T, d_in,
-                *_mx4_args(bases, rows, ys, workspace))
+                *_mx4_args(bases, _SIZES[len(rows)](*rows), ys, workspace))
 
 
 def bd_base_gemm_mx4x4_n_workspace_bytes(T: int, d_in: int, d_outs) -> int:
@@ -756,7 +760,7 @@ def bd_base_gemm_mx4x4_n(x_codes, x_scales, bases, ys, workspace=None, stream=No
     rows = _mx4_bases(bases, idx, d_in)
     _mx4_outs(ys, T, rows, workspace, idx)
     return _run(lib().bd_base_gemm_mx4x4_n, idx, stream, x_codes.data_ptr(), x_scales.data_ptr(), T,
-                d_in, *_mx4_args(bases, rows, ys, workspace))
+                d_in, *_mx4_args(bases, _SIZES[len(rows)](*rows), ys, workspace))
 
 
 def _tokens(tokens) -> int:
@@ -806,8 +810,9 @@ def _current(stream, t):
     allocates on t's device is that stream's, as under torch.cuda.stream."""
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(getattr(stream, "cuda_stream", stream))
+        dev = t.device if isinstance(t, torch.Tensor) and t.is_cuda else None  # (checked by the call)
         # (ExternalStream takes a handle of 0 for none and picks a stream from its pool)
-        stream = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 
@@ -844,13 +849,14 @@ def base_gemm_mx4(x: torch.Tensor, bases, ws=None, stream=None):
     idx, T, d_in = _tokens_2d(x, "x", (torch.bfloat16,))
     rows = _mx4_bases(bases, idx, d_in)
     ys = [x.new_empty((T, n), dtype=torch.float32) for n in rows]
+    sizes = _SIZES[len(rows)](*rows)
     if ws is None:
-        need = bd_base_gemm_mx4_n_workspace_bytes(T, d_in, rows)
+        need = lib().bd_base_gemm_mx4_n_workspace_bytes(T, d_in, len(rows), sizes)
         ws = workspace(need, x.device) if need > 0 else None
     else:
         _dev(ws, "workspace", None, None, x.device)
     _check(_run(lib().bd_base_gemm_mx4_n, idx, stream, x.data_ptr(), BD_BF16, T, d_in,
-                *_mx4_args(bases, rows, ys, ws)), "bd_base_gemm_mx4_n")
+                *_mx4_args(bases, sizes, ys, ws)), "bd_base_gemm_mx4_n")
     return ys
 
 
@@ -863,13 +869,14 @@ def base_gemm_mx4x4(xq, bases, ws=None, stream=None):
     idx, T, d_in = _mx4(x_codes, x_scales, "token")
     rows = _mx4_bases(bases, idx, d_in)
     ys = [x_codes.new_empty((T, n), dtype=torch.float32) for n in rows]
+    sizes = _SIZES[len(rows)](*rows)
     if ws is None:
-        need = bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, rows)
+        need = lib().bd_base_gemm_mx4x4_n_workspace_bytes(T, d_in, len(rows), sizes)
         ws = workspace(need, x_codes.device) if need > 0 else None
     else:
         _dev(ws, "workspace", None, None, x_codes.device)
     _check(_run(lib().bd_base_gemm_mx4x4_n, idx, stream, x_codes.data_ptr(), x_scales.data_ptr(), T,
-                d_in, *_mx4_args(bases, rows, ys, ws)), "bd_base_gemm_mx4x4_n")
+                d_in, *_mx4_args(bases, sizes, ys, ws)), "bd_base_gemm_mx4x4_n")
     return ys
 
 

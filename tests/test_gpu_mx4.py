@@ -265,6 +265,8 @@ def test_helpers_on_a_given_stream(as_int):
         d = (got != want[i]).nonzero()
         assert d.shape[0] == 0, (what, i, d.shape[0], float((got - want[i]).abs().max()), d[:8].tolist())
 
+    with pytest.raises(ValueError):
+        B.base_gemm_mx4(x.cpu(), [base], stream=stream)  # the call's own refusal, not the stream's
     for i, f in enumerate(calls):  # the default stream's handle is 0: in order with what follows
         for _ in range(10):
             same(i, f(torch.cuda.default_stream().cuda_stream), "default stream")
