@@ -284,6 +284,7 @@ k_mx4_rows(const void* __restrict__ x, const uint8_t* __restrict__ xs, const Gem
                     xr, ok ? (uint32_t)m * (uint32_t)(2 * K) + 64u * (uint32_t)(b0 + 4 * s) + 16u * j : kOOB);
         }
     }
+    __builtin_amdgcn_sched_barrier(0);  // (else products start between the loads, to save registers)
     f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
