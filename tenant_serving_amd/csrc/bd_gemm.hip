@@ -83,9 +83,11 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // Q8: W holds int8 codes with one scale per row (the INT8 base): each lane loads 16
 // codes of a row into registers two stages ahead (two register sets, alternating), widens
 // them to bf16 and writes the two chunks to their swizzled LDS slots after the products of
-// the stage before; the epilogue multiplies each row by its scale.  Each stage's code
-// loads go out before its token copies: vector loads complete in order, so waiting for
-// the codes leaves the younger token copies in flight and the ring keeps its depth.
+// the stage before; the epilogue multiplies each row by its scale.  A stage's code loads
+// are written before its token copies (vector loads complete in order: waiting for the
+// codes then leaves younger copies in flight), but the compiler places them among or
+// behind the copies, and on all tiles but 64 x 64 it also waits for every load at the top
+// of each second stage, so the INT8 ring runs less deep than the bf16 one.
 template <int BR, int BT, int BK, int NS, int NW, bool Q8>
 __global__ void __launch_bounds__(64 * NW)
 k_gemm(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, int ntt, int S, int kps) {
@@ -210,8 +212,12 @@ k_gemm(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, int ntt,
     using P0 = std::integral_constant<int, 0>;
     using P1 = std::integral_constant<int, 1>;
     // The prologue issues in the loop's order, as if by stages t = -max(NS - 1, 2) .. -1
-    // (stage t: stage t + 2's codes, then stage t + NS - 1's copies), so that the wait at the
-    // top of every stage counts the same younger loads as in the loop.
+    // (stage t: stage t + 2's codes, then stage t + NS - 1's copies).  bf16: copies alone,
+    // whose order holds, so the wait at the top of every stage counts the same younger loads
+    // as in the loop.  Q8: the compiler moves the register loads of codes among the copies,
+    // and no barrier here keeps a number of them behind a copy (on the 64 x 64 tile it put
+    // codes(1) last and codes(0) first: the counted wait of stage 0 then left a copy of
+    // stage 0 in flight), so the prologue's loads all land before the first stage.
 #pragma unroll
     for (int t = -(NS - 1 > 2 ? NS - 1 : 2); t < 0; ++t) {
         if constexpr (Q8) {
@@ -220,17 +226,22 @@ k_gemm(const uint16_t* __restrict__ x, const GemmMats gm, int T, int K, int ntt,
         }
         if (t + NS - 1 >= 0) issue(t + NS - 1);
     }
-    if constexpr (Q8) qstore(0, P0());
+    if constexpr (Q8) {
+        qstore(0, P0());
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    }
 
     const int m32 = lane & 31, h = lane >> 5;
     // stage s (parity pc: Q8 loads stage s + 2's codes into set pc and stores stage s + 1's
     // from the other set)
     auto stage = [&](int s, auto pc) {
         constexpr int P = decltype(pc)::value;
-        // this wave's copies of stage s are done (NS - 2 younger stages in flight, each one
-        // stage's token copies (bf16: and W copies; Q8: and the codes of a later stage));
-        // the barrier makes every wave's copies visible and frees the slot of stage s - 1
-        // (Q8: also this wave's LDS writes of the stage's codes)
+        // this wave's copies of stage s are done: stage s - NS + 1 of the loop sent them (the
+        // prologue's have landed, or are counted alike), and each of the NS - 2 stages since
+        // sent one stage's token copies (bf16: and W copies; Q8: and the codes of a later
+        // stage, anywhere between its own barrier and the next, which no load crosses), so
+        // kAhead loads at least are younger; the barrier makes every wave's copies visible
+        // and frees the slot of stage s - 1 (Q8: also this wave's LDS writes of the codes)
         constexpr int kAhead = ((Q8 ? kQInst : kWInst) + kXInst) * (NS - 2);
         __builtin_amdgcn_s_waitcnt((Q8 ? 0x0070 : 0x0F70) | (kAhead & 0xF) |
                                    (((kAhead >> 4) & 3) << 14));
