@@ -347,8 +347,10 @@ bd_status bd_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t
 /* Base products on MX4 rows of up to 4 matrices that read the same tokens:
  * y[t][o] = sum_i x[t][i] code[o][i] 2^E, fp32 sums (overwrites y).
  * bd_base_gemm_mx4_n takes bf16 tokens (BD_ERR_DTYPE otherwise); the weights are widened
- * to bf16 exactly on chip.  bd_base_gemm_mx4x4_n takes MX4 tokens (bd_quantize_mx4 of
- * x [T][d_in]); the products are exact in the block-scaled matrix instructions.
+ * to bf16 exactly on chip (a weight of 2^128 or more, which no block quantised from finite
+ * values holds, to Inf).  bd_base_gemm_mx4x4_n takes MX4 tokens (bd_quantize_mx4 of
+ * x [T][d_in]); the products are exact in the block-scaled matrix instructions, whatever
+ * the weight's size.
  *  n_mats       : 1..4.   d_outs : host int64[n_mats].
  *  w_codes, w_scales, ys : host arrays of n_mats device pointers; ys[i] fp32
  *                 [T][d_outs[i]], 16-byte aligned.

@@ -186,3 +186,17 @@ def test_apply_groups_and_wide_rows(case, tokens):
     assert np.all(g0[ids < 0] == 0)
     y2 = B.apply_mx4(x_dev, codes, scales, signs, dsc, p, ids_dev, y_dtype=ydt, tokens=tokens)
     assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("T", [5, 80])
+def test_products_of_values_beyond_the_range(T):
+    """Codes of 2 and more under byte 254 (2^128 and above; no block quantised from finite
+    values has them): the bf16-token product widens the weights to bf16, where they are Inf;
+    the MX4-token product never forms the value, and its sums are ordinary."""
+    base, wv = extreme_base(20, 576, 254, T)
+    g = torch.Generator().manual_seed(T)
+    x = (torch.randn(T, 576, generator=g).clamp(-3, 3) * 2.0 ** -120).bfloat16().to(DEV)
+    y, _ = product(False, x, base)
+    assert not torch.isfinite(y).any()
+    y4, xv = product(True, x, base)
+    assert_product(y4.cpu().numpy(), xv, wv, T)
