@@ -29,14 +29,14 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // ------------------------------------------------------------------ group
-// meta[0] status bits, meta[1] number of items, meta[2] number of tokens with
-// a valid user.  items[i] = {user, first sorted position, token count, 0};
-// suser[p] = user of sorted position p (p < meta[2]).
+// meta[0] status bits, meta[2] number of tokens with a valid user; suser[p] = user of
+// sorted position p (p < meta[2]).  The work items, items[i] = {user, first sorted position,
+// token count, 0}, and their number meta[1] come from k_tile_plan<true> after k_group and
+// from k_group_wave itself (grouped_by_wave says which kernels a batch takes).
 //
 // Sorting by counting: a token's place among the (user, token) keys is the number of keys
 // below its own.  A block takes 4 tokens, the 64 lanes of a wave share the count of one; block 0
-// also counts the valid tokens and writes the status (k_tile_plan then makes the items).  It
-// takes 4.7 us at 512 tokens and 5.2 us at 1144 (8.2 with 16 lanes to a token).
+// also counts the valid tokens and writes the status.  It takes 4.7 us at 512 tokens and 5.2 us at 1144 (8.2 with 16 lanes to a token).
 __global__ void __launch_bounds__(256)
 k_group(const int32_t* __restrict__ ids, int T, int U, int32_t* __restrict__ perm,
         int32_t* __restrict__ suser, uint32_t* __restrict__ meta) {
@@ -81,7 +81,8 @@ k_group(const int32_t* __restrict__ ids, int T, int U, int32_t* __restrict__ per
 
 // Batches of at most 64 tokens: one wave, no barriers.  Lane l holds key l;
 // a 64-lane bitonic network of shuffles sorts them, ballots find the segment
-// starts and prefix counts place the items.  Same outputs as k_group.
+// starts and prefix counts place the items.  Outputs: k_group's, and the items and meta[1],
+// which k_tile_plan<false> reads.
 __global__ void __launch_bounds__(64)
 k_group_wave(const int32_t* __restrict__ ids, int T, int U, int32_t* __restrict__ perm,
              int32_t* __restrict__ suser, int4* __restrict__ items, uint32_t* __restrict__ meta) {
@@ -474,7 +475,7 @@ hipError_t launch_batch_prepare(const BatchPlan& pl, const void* x, const int32_
                              hipMemcpyDeviceToDevice, s);
         return err != hipSuccess ? err : hipGetLastError();
     }
-    if (pl.T <= kGroupWaveT) {
+    if (grouped_by_wave(pl.T)) {
         hipLaunchKernelGGL(k_group_wave, dim3(1), dim3(64), 0, s, ids, (int)pl.T, pl.U,
                            (int32_t*)(batch + pl.off_perm), (int32_t*)(batch + pl.off_user),
                            (int4*)(batch + pl.off_items), meta);

@@ -1423,12 +1423,12 @@ hipError_t launch_tile_plan(const BatchPlan& bp, char* batch, hipStream_t s) {
     uint32_t* meta = (uint32_t*)(batch + bp.off_meta);
     int32_t *tiles = (int32_t*)(batch + bp.off_tiles), *torder = (int32_t*)(batch + bp.off_torder),
             *tpre = (int32_t*)(batch + bp.off_tpre);
-    if (bp.T > kGroupWaveT)
-        k_tile_plan<true><<<dim3(1), dim3(kPlanThreads), 0, s>>>(items, suser, meta, tiles, torder, tpre,
-                                                                 (int)bp.ntiles);
-    else
+    if (grouped_by_wave(bp.T))
         k_tile_plan<false><<<dim3(1), dim3(64), 0, s>>>(items, suser, meta, tiles, torder, tpre,
                                                         (int)bp.ntiles);
+    else
+        k_tile_plan<true><<<dim3(1), dim3(kPlanThreads), 0, s>>>(items, suser, meta, tiles, torder, tpre,
+                                                                 (int)bp.ntiles);
     return hipGetLastError();
 }
 

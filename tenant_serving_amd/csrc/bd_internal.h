@@ -69,7 +69,10 @@ hipError_t launch_select_axis(const AxisPlan& ap, const void* wf, const void* wb
 constexpr int kItemTokens = 32;   // max tokens of one (user, chunk) work item (<= 2 MFMA tiles)
 constexpr int kMaxMats = 4;       // matrices of one grouped launch (they share X)
 constexpr int kMaxGroupT = 8192;  // tokens of a prepared batch
-constexpr int kGroupWaveT = 64;   // ... that one wave groups and cuts into items (k_group_wave)
+// Batches of up to kGroupWaveT tokens: one wave groups them and cuts them into items
+// (k_group_wave, then k_tile_plan<false>); larger ones: k_group, then k_tile_plan<true>.
+constexpr int kGroupWaveT = 64;
+inline bool grouped_by_wave(int64_t T) { return T <= kGroupWaveT; }
 constexpr int kMaxUsers = (1 << 17) - 1;
 
 // Prepared batch (bd_batch_prepare): tokens grouped by user into work items; for
