@@ -179,7 +179,7 @@ bd_status bd_batch_prepare(const void* x, bd_dtype x_dtype, int64_t T, int64_t d
     bd_status st = make_batch_plan(T, n_users, d_in, x_dtype, &bp);
     if (st != BD_OK) return st;
     if (!batch || batch_bytes < bp.total || !aligned(batch, kAlign)) return BD_ERR_WORKSPACE;
-    if (T > 0 && (!x || !user_ids)) return BD_ERR_INVALID_ARG;
+    if (T > 0 && ((!x && x_dtype != BD_BF16) || !user_ids)) return BD_ERR_INVALID_ARG;
     if (T > 0 && (!aligned(x, 16) || !aligned(user_ids, 4))) return BD_ERR_INVALID_ARG;
     hipError_t e = launch_batch_prepare(bp, x, user_ids, (char*)batch, (hipStream_t)stream);
     return e == hipSuccess ? BD_OK : BD_ERR_DEVICE;
