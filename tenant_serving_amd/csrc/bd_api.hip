@@ -542,11 +542,13 @@ bd_status bd_base_gemm_mx4x4_n(const uint8_t* x_codes, const uint8_t* x_scales, 
 //  fused: decode batches of bf16 tokens, MATRIX or ROW scales, rows of up to 4096 columns: one
 //         launch (k_decode_unit on MX4 rows).
 //  decode: the other batches of at most 16 tokens but GROUP scales, up to kMx4DecodeRows
-//         rows: the base product with the decode path's two launches around it.  16 tokens
-//         of 16 users, d_in 4096, microseconds against the prepared batch: 4096 rows 30 to
-//         42, 12288 52 to 58, 16384 62 to 60, 28672 102 to 89; 2 tokens of one user at
-//         d_in 8192: 23 to 38, 42 to 45, 48 to 45, 77 to 57 (every 16 rows read all encoded
-//         tokens again, which the prepared batch's blocks of 256 rows do not).
+//         rows: the base product with the decode path's two launches around it.  Against
+//         the prepared batch at COL scales or MX4 tokens on 4096 columns and ROW scales on
+//         8192 and 14336, 1 to 16 tokens of 1 to 16 users, it takes 0.59-0.77 of the time on
+//         4096 rows, 0.75-0.89 on 8192, 0.78-0.99 on 12288, 0.99-1.12 on 16384, 1.08-1.47
+//         on 28672 (every 16 rows read all encoded tokens again, which the prepared batch's
+//         blocks of 256 rows do not): 16 tokens of 16 users, COL, 30 to 39 us on 4096 rows,
+//         105 to 87 on 28672.
 //  otherwise the prepared batch.
 constexpr int64_t kMx4DecodeRows = 12288;
 struct Mx4ApplyPlan {

@@ -187,7 +187,10 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[MI][NJ], float* y
 
 // One wave per 512-column segment of a row: a lane holds 8 consecutive columns, four
 // lanes one block.  `values` (may be null, may be w itself: a lane reads its columns
-// before it writes them) receives what the codes stand for.
+// before it writes them) receives what the codes stand for.  Bound by HBM: 4096 x 14336 with
+// the values 41.6 us from bf16 (6.4 TB/s), 91.9 from fp32 (5.5).  Rows that leave lanes of
+// their last segment without columns cost those lanes: at the same number of elements 52 us
+// in rows of 512 columns, 63 of 576, 184 of 64 (weights have thousands of columns).
 template <typename WT>
 __global__ void __launch_bounds__(64 * kQuantWaves)
 k_mx4_quantize(const WT* w, int64_t rows, int64_t cols, int64_t nseg, uint8_t* __restrict__ codes,
@@ -473,7 +476,8 @@ k_mx4_gemm4(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, cons
     // first stage before them the scales of the next period, spread evenly over its products.
     // (All at once, copies or reads hold up every wave's products while the address unit or
     // the LDS takes them in turn: 256 columns of a 256 x 256 block took 3600 cycles with the
-    // copies behind the barrier, 3250 with the reads alone in bursts, and take 2820 like this.)
+    // copies behind the barrier, 3250 with the reads alone in bursts, and take 2740 to 2850
+    // like this, of which the products alone take 2300.)
     auto products = [&](int s, auto kc, auto jc, int sn, auto nc) {
         constexpr int kk = decltype(kc)::value, J = decltype(jc)::value, O = J & 1;
         constexpr int kS = J == 0 ? kSInst : 0, kTot = kS + kD, M = kSteps * MI * NJ;
@@ -997,14 +1001,17 @@ k_mx4_reduce(const GemmMats gm, int T, int S) {
     }
 }
 
-// Tile and K split by a model of their time (us), fitted to 3700 measurements of the tiles
-// and splits at 17..8192 tokens on 700 x 1088 to 34816 x 5120 (graph replays on one MI355X):
+// Tile and K split by a model of their time (us), fitted to measurements of the tiles and
+// splits at 17..8192 tokens on 700 x 1088 to 34816 x 5120 (graph replays on one MI355X):
 //   a + max(ceil(blocks / (256 occ)) b, ceil(blocks / 256) c) n + (S > 1: 2 + bytes / 3.5 TB/s)
 // with n the 256-column steps of a block's K part, occ the blocks a CU holds, a the fixed
-// cost, b one block's time per step, c a CU's per block and step.  The choice is 1.7%
-// (MX4 tokens) and 2.5% (bf16) off the best measured on average, 17% and 32% at the worst;
-// always the largest tile, with its best split, would be 54% and 72% off on average, always
-// the smallest 19% and 22%.
+// cost, b one block's time per step, c a CU's per block and step.  Against every tile and
+// split on matrices and batches that the fit did not see (seven matrices, 24 to 6000 tokens),
+// the choice is 1.2% (MX4 tokens) and 1.9% (bf16) off the best on average, 18% and 16% at the
+// worst; always the largest tile, with its best split, is 42% and 57% off on average, always
+// the smallest 25% and 26%.  At 1, 8 and 16 tokens, where rows_fit and the model share the
+// choice: 4.9% and 2.2%, 27% (16 tokens on 10240 x 8192) and 21% (8 tokens on 6912 x 2560,
+// where the row kernel would win) at the worst.
 struct TileCost {
     int tile, br, bt, occ;
     double a, b, c;
