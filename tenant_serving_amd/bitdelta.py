@@ -1174,8 +1174,8 @@ def rmsnorm_fp8(h: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
 
 
 def base_gemm_fp8(xq, bases, y_dtype=torch.float32, ws=None, stream=None):
-    """[x . W^T] in y_dtype (fp32 or bf16) for 1..4 FP8 matrices (codes, scales) and FP8
-    tokens xq = (codes, scale bytes)."""
+    """[x . W^T] in y_dtype (fp32, or bf16: the fp32 sums rounded once) for 1..4 FP8 matrices
+    (codes, scales) and FP8 tokens xq = (codes, scale bytes)."""
     x_codes, x_scales = xq
     if stream is not None:
         with _current(stream, x_codes):

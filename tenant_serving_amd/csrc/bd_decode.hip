@@ -933,9 +933,9 @@ constexpr int kUnitRing = 8;
 // FP8: the base weight as FP8 rows (bd_fp8.hip; wscale: their block scales), half the base
 // bytes, and the tokens in FP8 too: xc and xs8 where they are given, else quantised by the wave
 // from the unit's tokens in LDS, the same codes (k_fp8_tokens).  A lane holds its 32 codes of a
-// token's 128 columns as the product takes them, so two ring items are one block-scaled
-// product, whose sums the block's weight scale multiplies.
-// 16 tokens of 16 users on 4096 x 4096: 15.8 us against 25.0 as quantiser, base product
+// token's 128 columns as the product takes them, so two ring items are one product of 128
+// columns (four bf16 products of the widened codes), whose sums the two blocks' scales multiply.
+// 16 tokens of 16 users on 4096 x 4096: 16.4 us against 25.0 as quantiser, base product
 // and decode path one after the other; 50 MB, 10.4 us at the rate of a large copy.
 enum { kBaseBf16 = 0, kBaseInt8 = 1, kBaseMx4 = 2, kBaseFp8 = 3 };
 template <int MODE, int FMT>
@@ -1245,9 +1245,10 @@ k_decode_unit(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, i
         // and 64 on from there of row m, as of token m; the ring holds the unit whole
         auto product = [&](auto qc) {
             constexpr int q = decltype(qc)::value;
-            const f32x4 p = mfma8<q>(join(ring[2 * q], ring[2 * q + 1]), join(xq[q][0], xq[q][1]), xe);
+            const f32x4 p = mfma128(widen32(ring[2 * q], ring[2 * q + 1]), widen32(xq[q][0], xq[q][1]));
+            const float f = product_scale<q>(sw[q], xe);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) accb[e] = 4 * wv + q < (int)((d_in + 127) / 128) ? __builtin_fmaf(p[e], sw[q], accb[e]) : accb[e];
+            for (int e = 0; e < 4; ++e) accb[e] = 4 * wv + q < (int)((d_in + 127) / 128) ? __builtin_fmaf(p[e], f, accb[e]) : accb[e];
         };
         product(std::integral_constant<int, 0>());
         product(std::integral_constant<int, 1>());

@@ -5,8 +5,7 @@
 // Codes are OCP e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa bits; largest 448), one
 // byte per element, row-major.  A weight has one fp32 scale per block of 128 x 128,
 // [ceil(rows / 128)][ceil(cols / 128)]; tokens have one power of two 2^E per 128 columns of
-// a row, the byte E + 127 (255: NaN) that the block-scaled matrix instructions take as it
-// is, in rows of 4 ceil(cols / 512) bytes with zeros past the last block, so that the scales
+// a row, the byte E + 127 (255: NaN), in rows of 4 ceil(cols / 512) bytes with zeros past the last block, so that the scales
 // of any 512 columns are one aligned dword.
 #include "bd_fp8.h"
 #include "bd_tiles.h"
@@ -16,7 +15,6 @@
 namespace bd {
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // 16 bytes at any element of y
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -356,7 +354,7 @@ hipError_t launch_rmsnorm_fp8(const void* h, int hdtype, const void* r, int rdty
 // eight partial tiles summed in LDS in wave order.  There is nothing to reuse at so few tokens:
 // every byte of Wq goes from memory to the registers of the one wave that multiplies it, and
 // the time is the latency of one such round beside the bytes' (1 token on 4096 + 1024 + 1024
-// rows of 4096: 8.3 us for 25 MB, 5.2 at the rate of a large copy).
+// rows of 4096: 9.4 us for 25 MB, 5.2 at the rate of a large copy).
 constexpr int kRowsWaves = 8, kRowsMaxT = 64;
 template <int NT>
 __global__ void __launch_bounds__(64 * kRowsWaves)
@@ -400,19 +398,21 @@ k_fp8_rows(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const 
             xe[j] = buf_load4(er, t < T ? 4u * (uint32_t)(t * nu + u) : kOOB);
         }
         __builtin_amdgcn_sched_barrier(0);  // (every load before the first product)
+        auto block = [&](auto qc) {
+            constexpr int q = decltype(qc)::value;
+            const Wide w = widen32(W[q][0], W[q][1]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            f32x4 p[4];
-            p[0] = mfma8<0>(join(W[0][0], W[0][1]), join(X[j][0][0], X[j][0][1]), xe[j]);
-            p[1] = mfma8<1>(join(W[1][0], W[1][1]), join(X[j][1][0], X[j][1][1]), xe[j]);
-            p[2] = mfma8<2>(join(W[2][0], W[2][1]), join(X[j][2][0], X[j][2][1]), xe[j]);
-            p[3] = mfma8<3>(join(W[3][0], W[3][1]), join(X[j][3][0], X[j][3][1]), xe[j]);
+            for (int j = 0; j < NT; ++j) {
+                const f32x4 p = mfma128(w, widen32(X[j][q][0], X[j][q][1]));
+                const float f = product_scale<q>(sw[q], xe[j]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] = 4 * u + q < nb ? __builtin_fmaf(p[q][e], sw[q], acc[j][e]) : acc[j][e];
-        }
+                for (int e = 0; e < 4; ++e) acc[j][e] = 4 * u + q < nb ? __builtin_fmaf(p[e], f, acc[j][e]) : acc[j][e];
+            }
+        };
+        block(std::integral_constant<int, 0>());
+        block(std::integral_constant<int, 1>());
+        block(std::integral_constant<int, 2>());
+        block(std::integral_constant<int, 3>());
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) red[j][wv][lane] = acc[j];
@@ -432,18 +432,19 @@ k_fp8_rows(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const 
 }
 
 // The product for larger batches: block tiles of BR rows of Wq x BT tokens, NWR x NWT waves,
-// each a block of RI x TJ tiles of v_mfma_scale_f32_16x16x128_f8f6f4, one per block of 128
-// columns.  A product's sums p over those columns already carry the tokens' scales; the
-// weight's scale, one per wave and 128 columns (a wave's rows lie in one block of 128 rows),
-// enters as acc = p sw + acc, the fma of a product issued two products later, when the matrix
+// each a block of RI x TJ tiles of 16 x 16, a product of 128 columns at a time as four
+// v_mfma_f32_16x16x32_bf16 on the codes widened to bf16 (mfma128: why not the FP8 instructions).
+// A product's sums p are without scales; sw 2^E, the weight's scale (one per wave and 128
+// columns: a wave's rows lie in one block of 128 rows) times the lane's token's, enters as
+// acc = p (sw 2^E) + acc, the fma of a group of tiles issued one group later, when the matrix
 // unit has left its result.
 // K advances one block of 128 columns per stage (128 bytes of a row) through a ring of NS LDS
 // stages filled by buffer loads that write LDS directly; 16-byte chunks are swizzled in their
 // row so that 16 rows read at one chunk hit all banks.  A wave holds its tokens' operands of a
-// stage and reads its W rows 16 at a time, one ahead of the products.  Behind the last read of
-// a stage stands its one barrier: it frees the stage's slot, whose copies of stage s + NS go
-// out one per product from there on, and shows stage s + 1, whose token operands take the
-// places of those that the last row of products leaves.
+// stage in bf16 and reads its W rows 16 at a time, one row ahead of the products.  Behind the
+// last read of a stage stands its one barrier: it frees the stage's slot, whose copies of stage
+// s + NS go out from there on, and shows stage s + 1, whose token codes are read then and
+// widened into the places of the operands that the products leave.
 // Token scales come 512 columns (one dword a token) at a time into a ring of two slots.
 // S > 1: K part sp covers columns [sp kps, (sp + 1) kps) (kps a multiple of 512) and writes
 // its partial tile to part.
@@ -451,23 +452,24 @@ k_fp8_rows(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const 
 // second) of their 32, so that a lane ends up with 8 consecutive rows of its token and stores
 // them as 16 bytes; the swizzle of W's chunks takes the bits by which 16 such rows differ.
 //
-// Bound, large batches: the LDS port, the matrix unit and their power.  8192 tokens on 14336 x
-// 4096, bf16 out: 405 us, 2375 TFLOP/s, where a library's product with one scale per matrix
-// reached 2500 to 2750.  A stage of 256 x 256 takes 2730 cycles, 2050 of them the products' own
-// and as many the port's (192 KB read and 64 KB written at 128 bytes a cycle), with or without
-// memory behind the copies (2710); without the fmas 2520.  On random data the clock falls from
-// 2.4 to 1.8 GHz (codes of zero: 325 us).
-// Middling batches: 1144 tokens on 5120 x 17408, 240 tiles on 256 CUs, 114 us; tiles of 192
-// tokens, because 6 of them cover 1144 where 9 of 128 or 5 of 256 would leave a second round or
-// a fifth of the work empty (128 x 256 126 us); 1350 cycles a stage, 770 the products' and 1340
-// the port's.  Four waves with larger blocks read less LDS, but hid too little (1380 cycles for
-// 128 x 128 against 1050); reading a stage ahead into registers took 2% off the cycles, no more.
+// Large batches: the matrix unit at the bf16 rate and the vector instructions beside it.  On a
+// wave's 64 x 64 a stage is 64 products (16 cycles each) and 232 vector instructions (4 each),
+// 128 of them widen; the same mix run from registers alone, without LDS, reached 1600 TFLOP/s, a
+// library's bf16 product 1391 to 1458.  8192 tokens on 14336 x 4096, fp32 out: 830 to 875 us,
+// 1100 to 1160 TFLOP/s; 780 where the copies bring nothing from memory, 720 with the codes taken
+// as they are (no widening).  Less ordering between the instructions, chains of one tile, or two
+// blocks of four waves a CU: within 2%.  Wave tiles of 128 x 64 leave no registers for the
+// widened operands.
+// Middling batches: 1144 tokens on 5120 x 17408, 240 tiles of 128 x 192 on 256 CUs, 192 us (1060
+// TFLOP/s; 160 without widening): 6 tiles of 192 tokens cover 1144 where 9 of 128 or 5 of 256
+// would leave a second round or a fifth of the work empty (128 x 256 221 us).
 // Few tokens: the bytes of Wq.
 template <int BR, int BT, int NS, int NWR, int NWT, bool H>
 __global__ void __launch_bounds__(64 * NWR * NWT)
 k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const GemmMats gm, int T, int K,
            int ntt, int S, int kps, int GR, int tiles) {
     constexpr int NW = NWR * NWT, RI = BR / NWR / 16, TJ = BT / NWT / 16, M = RI * TJ;
+    constexpr int G = TJ % 2 == 0 ? 2 : TJ, NG = TJ / G;  // tiles of a group, groups of a row
     constexpr int kStage = (BR + BT) * 128, kSSlot = (BT < 64 ? 64 : BT) * 4;
     constexpr int kWInst = BR / 8 / NW, kXInst = BT / 8 / NW, kD = kWInst + kXInst;
     constexpr int kSI = (BT + 63) / 64;  // copies of a period's scales, a wave each (in turn)
@@ -481,7 +483,7 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
     }();
     constexpr int kStores = H ? M / 2 : M;
     static_assert(BR % (8 * NW) == 0 && BT % (8 * NW) == 0, "whole copy instructions per wave");
-    static_assert(BR % (16 * NWR) == 0 && BT % (16 * NWT) == 0 && M % 4 == 0 && RI % 2 == 0, "whole tiles");
+    static_assert(BR % (16 * NWR) == 0 && BT % (16 * NWT) == 0 && RI % 2 == 0 && G <= 3, "whole tiles");
     static_assert(128 % (BR / NWR) == 0, "a wave's rows share one scale");
     static_assert(NS >= 2 && NS <= 5, "a period's scales land before they are read");
     static_assert(kSI <= NW, "a wave copies one piece of the scales");
@@ -577,14 +579,15 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
     const int mw = H ? 8 * (m >> 2) + (m & 3) : m;
     const int offw[2] = {mw * 128 + 16 * (g ^ swzw(mw)), H ? (mw + 4) * 128 + 16 * (g ^ swzw(mw + 4)) : off};
     f32x4 acc[RI][TJ];
-    u32x4 A[2][2], Bv[TJ][2];
+    u32x4 A[2], Bv[TJ][2];  // codes: of the next 16 rows; of the next stage's tokens
+    Wide AW, XW[TJ];        // ... and in bf16: of these rows, of this stage's tokens
     uint32_t xe[TJ];
-    f32x4 P[4];
-    float sw[4], swl;  // a period's weight scales; that of the stage before
+    f32x4 P[2][G];
+    float sw[4], f[TJ], fl[G];  // a period's weight scales; this stage's; those of the last group before it
     auto read_a = [&](int slot, int i) {
         const char* p = smem + slot * kStage + (wr * (BR / NWR) + (H ? i / 2 * 32 : 16 * i)) * 128;
         const int o = offw[i & 1];
-        A[i & 1][0] = *(const u32x4*)(p + o), A[i & 1][1] = *(const u32x4*)(p + (o ^ 64));
+        A[0] = *(const u32x4*)(p + o), A[1] = *(const u32x4*)(p + (o ^ 64));
     };
     auto read_b = [&](int slot, int j) {
         const char* p = smem + slot * kStage + (BR + wt * (BT / NWT) + 16 * j) * 128;
@@ -597,7 +600,18 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
 #pragma unroll
         for (int q = 0; q < 4; ++q) sw[q] = wsc[4 * p + q < nbl ? 4 * p + q : nbl];
     };
-    // Stage s in slot `slot` (s % 4 == J), stage s + 1 in slot `next`.
+    // Columns 32 q .. of the operands (of the order in which the products take them)
+    auto widen_a = [&](int q) {
+        AW.q[q] = (q & 1) ? widen_bf16(A[q / 2].z, A[q / 2].w) : widen_bf16(A[q / 2].x, A[q / 2].y);
+    };
+    auto widen_x = [&](int j, int q) {
+        XW[j].q[q] = (q & 1) ? widen_bf16(Bv[j][q / 2].z, Bv[j][q / 2].w) : widen_bf16(Bv[j][q / 2].x, Bv[j][q / 2].y);
+    };
+    // Stage s in slot `slot` (s % 4 == J), stage s + 1 in slot `next`.  A row of 16 goes through
+    // the wave's tokens in groups of G tiles, each four products of 32 columns for the group's
+    // tiles in turn.  Between them stand, a step at a time, what later ones need: the reads, the
+    // copies, the widening of the next row's and the next group's operands into the registers
+    // that the products leave, and the scaled sums of the group before.
     auto stage = [&](int s, int slot, int next, auto jc) {
         constexpr int J = decltype(jc)::value;
         const int prev = slot == 0 ? NS - 1 : slot - 1;  // the slot that stage s - 1 left
@@ -609,33 +623,72 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
                 __builtin_amdgcn_s_barrier();
                 if constexpr (J == 0) copy_scales(s / 4 + 1);
             }
-            const i32x8 a8 = join(A[i & 1][0], A[i & 1][1]);
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                const int n = i * TJ + j, k = i == RI - 1 ? j : n + TJ;  // this product, from the barrier on
-                __builtin_amdgcn_sched_barrier(0);
-                P[n & 3] = mfma8<J>(a8, join(Bv[j][0], Bv[j][1]), xe[j]);
-                __builtin_amdgcn_sched_barrier(0);
-                if (j == 0) read_a(i == RI - 1 ? next : slot, (i + 1) % RI);
-                if (i == RI - 1) {
-                    read_b(next, j);
-                    if constexpr (J == 3) read_e(s / 4 + 1, j);
-                }
+            for (int gj = 0; gj < NG; ++gj) {
+                const int pp = (i * NG + gj) & 1;
 #pragma unroll
-                for (int c = 0; c < kD; ++c)
-                    if (at(c) == k) {
-                        if (i == RI - 1) copy(s + NS, slot, c);
-                        else copy(s - 1 + NS, prev, c);
+                for (int q = 0; q < 4; ++q) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int h = 0; h < G; ++h) {
+                        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                        P[pp][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(AW.q[q], XW[gj * G + h].q[q],
+                                                                           q == 0 ? zero : P[pp][h], 0, 0, 0);
                     }
-                // the product before the last
-                const int o = (n + M - 2) % M;
-                const float f = n >= 2 ? sw[J] : swl;
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (q == 0) {
+                        if (gj == 0) read_a(i == RI - 1 ? next : slot, (i + 1) % RI);
+                        if (i == RI - 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[o / TJ][o % TJ][e] = __builtin_fmaf(P[(n + 2) & 3][e], f, acc[o / TJ][o % TJ][e]);
+                            for (int h = 0; h < G; ++h) {
+                                read_b(next, gj * G + h);
+                                if constexpr (J == 3) read_e(s / 4 + 1, gj * G + h);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < G; ++h) {
+                        const int j = gj * G + h, n = i * TJ + j, k = i == RI - 1 ? j : n + TJ;  // this product, from the barrier on
+                        if (q == (h == 0 ? 1 : 3)) {
+#pragma unroll
+                            for (int c = 0; c < kD; ++c)
+                                if (at(c) == k) {
+                                    if (i == RI - 1) copy(s + NS, slot, c);
+                                    else copy(s - 1 + NS, prev, c);
+                                }
+                        }
+                        // the group before: i * NG + gj - 1, at first the last of stage s - 1
+                        if (q == 1 + h) {
+                            const int o = (n + M - G) % M;
+                            const float sc = i + gj == 0 ? fl[h] : f[o % TJ];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[o / TJ][o % TJ][e] = __builtin_fmaf(P[pp ^ 1][h][e], sc, acc[o / TJ][o % TJ][e]);
+                        }
+                        // the next group's tokens: in the first row this stage's, behind the last
+                        // row's last group the next stage's
+                        if (i == 0 && gj + 1 < NG) widen_x(j + G, q);
+                        if (i == RI - 1 && gj == NG - 1 && NG > 1) widen_x(h, q);
+                    }
+                    if (gj == NG - 1 && NG > 1) widen_a(q);
+                    if (NG == 1 && q == 3) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            widen_a(k);
+#pragma unroll
+                            for (int h = 0; h < G; ++h)
+                                if (i == RI - 1) widen_x(h, k);
+                        }
+                    }
+                    if (i + gj == 0 && q == 3) {
+#pragma unroll
+                        for (int j = 0; j < TJ; ++j) f[j] = product_scale<J>(sw[J], xe[j]);
+                    }
+                }
             }
         }
-        swl = sw[J];
+#pragma unroll
+        for (int h = 0; h < G; ++h) fl[h] = f[TJ - G + h];
         if constexpr (J == 3) read_sw(s / 4 + 1);
     };
     // The finished tile at rows o0, tokens u0 of y [T][N]: lane m + 16 g holds token m of each
@@ -689,7 +742,6 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
     for (;;) {
         __builtin_amdgcn_s_barrier();
         read_sw(0);
-        swl = 0.f;
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
             read_b(0, j);
@@ -701,7 +753,13 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
 #pragma unroll
             for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 2; q < 4; ++q) P[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int h = 0; h < G; ++h) P[1][h] = f32x4{0.f, 0.f, 0.f, 0.f}, fl[h] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            widen_a(q);
+#pragma unroll
+            for (int h = 0; h < G; ++h) widen_x(h, q);
+        }
         int slot = 0;
         auto one = [&](int s, auto jc) {
             const int next = slot == NS - 1 ? 0 : slot + 1;
@@ -715,10 +773,10 @@ k_fp8_gemm(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xsc, const
             if (s + 3 < nk) one(s + 3, std::integral_constant<int, 3>());
         }
 #pragma unroll
-        for (int o = M - 2; o < M; ++o)
+        for (int h = 0; h < G; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc[o / TJ][o % TJ][e] = __builtin_fmaf(P[o & 3][e], swl, acc[o / TJ][o % TJ][e]);
+                acc[RI - 1][TJ - G + h][e] = __builtin_fmaf(P[1][h][e], fl[h], acc[RI - 1][TJ - G + h][e]);
         // The next tile's first copies go out before this tile's stores (the empty copies past
         // the end have landed, and every wave has read what it will).
         const MatId done = mt;
@@ -756,8 +814,8 @@ struct Fp8Launch {
 };
 
 // Row tiles an XCD takes together: 8 from 8 token tiles on (its 32 blocks then share 8 + 4
-// operand tiles: 14336 x 4096 at 8192 tokens, fp32 out, 452 us against 457 with 4 and 471 with
-// 2; 8192 x 8192 458, 469 and 493), else 1.
+// operand tiles: 8192 x 8192 at 8192 tokens, fp32 out, 966 to 995 us against 1005 with 4 and 1087
+// with 1; 14336 x 4096 872 to 876, 869 and 897), else 1.
 inline int fp8_row_group(int ntt) { return ntt >= 8 ? 8 : 1; }
 
 template <int BR, int BT, int NS, int NWR, int NWT>
@@ -782,38 +840,41 @@ hipError_t launch_gemm(const Fp8Launch& l) {
 }
 
 // Kernel, tile and K split by a model of their time (us), fitted to measurements at 1..8192
-// tokens on twenty sets of matrices, 300 x 8192 to 34816 x 5120 (graph replays on one MI355X).
+// tokens on 26 sets of matrices, 300 x 8192 to 34816 x 5120 (graph replays on one MI355X).
 // Tiles, with n the 128-column stages of a block's K part and `blocks` of them, occ at a time
 // on a CU, in rounds of 256 occ (the last of what is left):
 //   a + max(sum over rounds of max(b n + e, the round's share of W / 5.9 TB/s),
-//           ceil(blocks / 256) (c n + f)) + (S > 1: 1.85 + bytes of the parts / 3.27 TB/s)
-// k_fp8_rows: a block's time grows with its tokens, and from some 160 to 190 row tiles on with
-// their number (2560 x 2560: 4.2 us at 1 token, 6.6 at 32, 9.6 at 64, against 9.0, 9.4 and 9.8
-// of the best tile; 4096 x 4096: 6.5, 10.2 and 14.6 against 9.7, 10.7 and 12.0).
-// Against every kernel, tile and split, on 90 sets of up to four matrices and batches of which
-// the fit saw few, the choice is 1.2% off the best on average: 1.6% up to 16 tokens (32% at the
-// worst, 6 tokens on 107 x 12352), 0.1% up to 64, 0.7% up to 512 and 1.9% above (8%).  Always
-// the 64 x 64 tile with its best split is 22% off on average, always 256 x 256 74%.
-enum { kRows, k256x256, k256x128, k128x256, k128x128, k64x64, k128x32, k64x32, k256x192, k128x192, k128x64 };
+//           ceil(blocks / 256) (c n + f)) + (S > 1: 3.03 + bytes of the parts / 3.84 TB/s)
+// k_fp8_rows: a block's waves go through K in turns of 4096 columns, which wait for memory
+// (l + q T each) until the row tiles are so many that all of W's flow takes longer:
+//   a + max(turns (l + q T), row tiles K / 4096 (r + p T) + z)
+// (2304 x 2304: 4.5 us at 1 token, 6.4 at 24, 10.4 at 64 against 13.0 of the best tile at 96;
+// 12288 x 4096: 14.0 at 6 tokens, and at 16 the best tile's 16.1.)
+// Against every kernel, tile and split, on eight other sets of matrices and twelve batches, the
+// choice is 0.1% off the best on average up to 16 tokens (8% at the worst, 16 tokens on 4096 x
+// 11008), 1.4% up to 64 (9%), 0.7% up to 384 (14%) and 0.8% above (5%).
+enum { kRows, k256x192, k256x128, k128x256, k128x192, k128x128, k64x128, k128x64, k64x64, k128x32, k64x32 };
 struct TileCost {
     int tile, br, bt, occ;
     double a, b, e, c, f;
 };
 constexpr TileCost kCost[] = {
-    {k256x256, 256, 256, 1, 3.37, 1.31, 10.5, 0.014, 2.37},
-    {k256x192, 256, 192, 1, 0.519, 1.13, 9.63, 0.003, 14.9},
-    {k256x128, 256, 128, 1, 0.0, 0.838, 8.5, 0.777, 10.2},
-    {k128x256, 128, 256, 1, 0.066, 0.784, 10.4, 0.898, 0.908},
-    {k128x192, 128, 192, 1, 0.937, 0.632, 8.42, 0.22, 0.042},
-    {k128x128, 128, 128, 1, 1.58, 0.52, 5.22, 0.123, 0.403},
-    {k128x64, 128, 64, 1, 3.22, 0.376, 2.66, 0.137, 0.025},
-    {k64x64, 64, 64, 2, 3.24, 0.325, 0.263, 0.241, 1.44},
-    {k128x32, 128, 32, 1, 1.66, 0.342, 3.34, 0.093, 0.024},
-    {k64x32, 64, 32, 4, 3.47, 0.297, 0.0, 0.208, 0.605}};
-struct RowsCost {  // k_fp8_rows<1, 2, 4>: a + units (l + q T) max(1, row tiles / r)
-    double a, l, q, r;
+    {k256x192, 256, 192, 1, 0.243, 1.9, 12.7, 0.03, 16.2},
+    {k256x128, 256, 128, 1, 0.558, 1.49, 10.3, 0.58, 4.09},
+    {k128x256, 128, 256, 1, 0.653, 1.4, 9.73, 0.537, 1.57},
+    {k128x192, 128, 192, 1, 0.119, 1.19, 7.83, 0.246, 0.141},
+    {k128x128, 128, 128, 1, 1.13, 0.931, 5.5, 0.104, 0.275},
+    {k64x128, 64, 128, 1, 3.86, 0.67, 2.77, 0.084, 0.02},
+    {k128x64, 128, 64, 1, 3.04, 0.631, 3.45, 0.059, 0.046},
+    {k64x64, 64, 64, 2, 2.76, 0.499, 0.48, 0.341, 1.53},
+    {k128x32, 128, 32, 1, 1.03, 0.579, 2.95, 0.044, 0.028},
+    {k64x32, 64, 32, 4, 3.58, 0.752, 0.169, 0.189, 0.759}};
+struct RowsCost {  // k_fp8_rows<1, 2, 4>
+    double a, l, q, r, p, z;
 };
-constexpr RowsCost kRowsCost[] = {{2.53, 1.76, 0.026, 166.0}, {3.52, 1.71, 0.063, 155.0}, {3.31, 4.23, 0.041, 134.0}};
+constexpr RowsCost kRowsCost[] = {{2.99, 2.01, 0.08, 0.0124, 3.43e-4, 0.59},
+                                  {3.36, 2.73, 0.0793, 0.0172, 4.1e-4, 1.04},
+                                  {4.0, 3.79, 0.0716, 0.0202, 4.41e-4, 1.54}};
 struct Fp8Plan {
     int tile, S;
     int64_t kps;
@@ -828,10 +889,9 @@ Fp8Plan plan_fp8(int64_t T, int64_t d_in, const int64_t* d_outs, int n, bool spl
     double best = 1e30;
     if (T <= kRowsMaxT) {
         const RowsCost& c = kRowsCost[T <= 16 ? 0 : T <= 32 ? 1 : 2];
-        const double units = d_in < 512 * kRowsWaves ? (double)d_in / (512 * kRowsWaves)
-                                                     : (double)((d_in + 512 * kRowsWaves - 1) / (512 * kRowsWaves));
-        const double fill = (double)row_tiles / c.r;
-        best = c.a + units * (c.l + c.q * (double)T) * (fill > 1.0 ? fill : 1.0);
+        const double units = (double)d_in / (512 * kRowsWaves), turns = units > 1.0 ? (double)((d_in + 512 * kRowsWaves - 1) / (512 * kRowsWaves)) : units;
+        const double wait = turns * (c.l + c.q * (double)T), flow = (double)row_tiles * units * (c.r + c.p * (double)T) + c.z;
+        best = c.a + (wait > flow ? wait : flow);
     }
     const double stream = (double)(N * d_in) / 5.9e6;
     for (const TileCost& t : kCost) {
@@ -849,7 +909,7 @@ Fp8Plan plan_fp8(int64_t T, int64_t d_in, const int64_t* d_outs, int n, bool spl
             double us = (double)whole * full + (last > one ? last : one);
             const double cu = (double)((blocks + 255) / 256) * (t.c * stages + t.f);
             us = t.a + (us > cu ? us : cu);
-            if (parts > 1) us += 1.85 + (double)(T * N * 4 * (parts + 1)) / 3.27e6;
+            if (parts > 1) us += 3.03 + (double)(T * N * 4 * (parts + 1)) / 3.84e6;
             if (us < best) {
                 best = us;
                 pl = {t.tile, (int)parts, kps};
@@ -910,15 +970,15 @@ hipError_t launch_fp8_product(const uint8_t* x, const uint8_t* xscales, int64_t 
             e = hipGetLastError();
             break;
         }
-        case k256x256: e = launch_gemm<256, 256, 2, 2, 4>(l); break;
-        case k256x128: e = launch_gemm<256, 128, 3, 2, 4>(l); break;
+        case k256x192: e = launch_gemm<256, 192, 2, 2, 4>(l); break;
+        case k256x128: e = launch_gemm<256, 128, 3, 4, 2>(l); break;
         case k128x256: e = launch_gemm<128, 256, 3, 2, 4>(l); break;
+        case k128x192: e = launch_gemm<128, 192, 3, 2, 4>(l); break;
         case k128x128: e = launch_gemm<128, 128, 3, 2, 4>(l); break;
+        case k64x128: e = launch_gemm<64, 128, 4, 2, 4>(l); break;
         case k128x64: e = launch_gemm<128, 64, 4, 4, 2>(l); break;
         case k64x64: e = launch_gemm<64, 64, 4, 2, 2>(l); break;
         case k128x32: e = launch_gemm<128, 32, 4, 4, 1>(l); break;
-        case k256x192: e = launch_gemm<256, 192, 2, 4, 2>(l); break;
-        case k128x192: e = launch_gemm<128, 192, 3, 4, 2>(l); break;
         default: e = launch_gemm<64, 32, 3, 2, 1>(l); break;
     }
     if (e != hipSuccess || pl.S == 1) return e;
