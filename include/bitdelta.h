@@ -457,6 +457,9 @@ bd_status bd_rmsnorm_fp8(const void* h, bd_dtype h_dtype, const void* residual,
  * (overwrites y).  Two codes multiply exactly and the sums are fp32: on Gaussian data and on
  * activations with loud channels y is within 2e-7 of its norm at up to 17408 columns, and a small
  * product beside large ones that cancel is kept as in any fp32 sum.
+ * A block's two scales meet as w_scale 2^E before its sum does: that product, and not each of
+ * them, is to be a normal fp32 number (below 2^-126 it loses bits; from 2^128 on it is Inf, and
+ * the outputs that multiply the block are not finite).
  *  x_codes, x_scales : as bd_quantize_fp8_tokens (T rows of d_in).
  *  n_mats            : 1..4.   d_outs : host int64[n_mats].
  *  w_codes, w_scales, ys : host arrays of n_mats device pointers; ys[i] [T][d_outs[i]] of
