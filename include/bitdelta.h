@@ -436,7 +436,8 @@ bd_status bd_dequantize_fp8(const uint8_t* codes, const float* scales, int64_t r
  * read: bf16 for the users' deltas, FP8 for the base.  Per token, with s = h + residual
  * (fp32, rounded to h's dtype; s = h without a residual):
  *     x = s / sqrt(mean(s^2) + eps) * weight     (fp32, rounded once to bf16)
- * and codes, scales as bd_quantize_fp8_tokens of that x.
+ * of any finite s (squares outside fp32's range are taken in scaled units), and codes, scales
+ * as bd_quantize_fp8_tokens of that x.
  *  h         : [T][d] of h_dtype (BD_F32 or BD_BF16), the residual stream.
  *  residual  : [T][d] of residual_dtype (BD_F32 or BD_BF16), a block's output, or NULL.
  *  weight    : [d] of weight_dtype (BD_F32 or BD_BF16).

@@ -198,7 +198,8 @@ k_fp8_dequantize(const uint8_t* __restrict__ codes, const float* __restrict__ sc
 // h's type first and the norm is that of the stored value, so that the call equals an
 // addition and a norm one after the other; x = s rsqrt(mean s^2 + eps) g in fp32, rounded to
 // bf16 once; the codes are those of the rounded x (k_fp8_tokens).  A thread reads its columns of
-// h and r before it writes them, so that h_out may be either.  Bound by HBM, one pass: 8192 x
+// h and r before it writes them, so that h_out may be either.  Rows whose squares leave fp32's
+// range (beyond 1e-15 or 1e19) are scaled by a power of two first.  Bound by HBM, one pass: 8192 x
 // 5120 of bf16 with an fp32 residual in 81 us (462 MB, 5.7 TB/s); one row of 4096 in 3.1 us,
 // where the sum across the block's waves is what there is to wait for.
 template <typename HT, int V>
@@ -237,18 +238,49 @@ k_rmsnorm_fp8(const HT* h, const void* r, int r_bf16, const void* __restrict__ g
             if (col < d) store8_keep(h_out + row + col, f[v]);
         }
     }
-    float sum = 0.f;
+    auto squares = [&]() {  // of the row, the same in every thread
+        float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += f[v][i] * f[v][i];
+            for (int i = 0; i < 8; ++i) sum += f[v][i] * f[v][i];
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-    if ((tid & 63) == 0) red[tid >> 6] = sum;
-    __syncthreads();
-    sum = red[0];
-    for (int w = 1; w < nt / 64; ++w) sum += red[w];
-    const float rstd = rsqrtf(sum / (float)d + eps);
+        for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
+        if ((tid & 63) == 0) red[tid >> 6] = sum;
+        __syncthreads();
+        sum = red[0];
+        for (int w = 1; w < nt / 64; ++w) sum += red[w];
+        return sum;
+    };
+    const float sum = squares();
+    float ms = sum / (float)d + eps;
+    // Squares that left fp32's range (a sum under 2^-100 may lack those under 2^-126): the row
+    // again in units of 2^k, k the exponent of its largest magnitude or of sqrt(eps).  (uniform)
+    if (sum < 0x1p-100f || !(sum < INFINITY) || !(ms < INFINITY)) {
+        uint32_t a = 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a = umax(a, amax8(f[v]));
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) a = umax(a, (uint32_t)__shfl_xor((int)a, m));
+        __syncthreads();
+        if ((tid & 63) == 0) red[tid >> 6] = __uint_as_float(a);
+        __syncthreads();
+        for (int w = 0; w < nt / 64; ++w) a = umax(a, __float_as_uint(red[w]));
+        if ((a | __float_as_uint(eps)) != 0u && a < 0x7F800000u) {  // (0 / 0, Inf and NaN stay what they are)
+            int e = -2 * 149, k = e;
+            if (a != 0u) (void)frexpf(__uint_as_float(a), &k);
+            if (eps != 0.f) (void)frexpf(eps, &e);
+            e = (e + 1) >> 1;
+            k = e > k ? e : k;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[v][i] = ldexpf(f[v][i], -k);
+            __syncthreads();
+            ms = squares() / (float)d + ldexpf(eps, -2 * k);
+        }
+    }
+    const float rstd = rsqrtf(ms);
     const int nb = (d + 127) / 128, ld = (d + 511) / 512 * 4;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
