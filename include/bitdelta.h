@@ -417,7 +417,8 @@ size_t bd_fp8_scale_stride(int64_t cols);
  * holding a NaN or Inf gets scale NaN and codes 0, so that every product with it is NaN.
  * values_out (may be NULL, may be w itself): [rows][cols] of w's dtype, what the codes stand
  * for (Inf for a |w| of 1.9375 2^127 or more, which rounds to 2^128), which is the W_base to
- * compress a user's delta against.  rows == 0 is a no-op. */
+ * compress a user's delta against.  Under 2^24 blocks of 128 x 128 (BD_ERR_UNSUPPORTED).
+ * rows == 0 is a no-op. */
 bd_status bd_quantize_fp8(const void* w, bd_dtype dtype, int64_t rows, int64_t cols,
                           uint8_t* codes_out, float* scales_out, void* values_out, void* stream);
 
@@ -467,8 +468,8 @@ bd_status bd_rmsnorm_fp8(const void* h, bd_dtype h_dtype, const void* residual,
  *                      y_dtype (BD_F32, to add the users' deltas to, or BD_BF16, rounded
  *                      once), 16-byte aligned.
  *  workspace         : as bd_base_gemm_mx4_n.
- * T == 0 is a no-op; d_in is a multiple of 64; one operand is under 2^31 bytes, d_in at most
- * and d_outs[i] under 2^22 (BD_ERR_UNSUPPORTED). */
+ * T == 0 is a no-op; d_in is a multiple of 64; one operand is under 2^31 bytes, T under 2^20,
+ * d_in at most and d_outs[i] under 2^22 (BD_ERR_UNSUPPORTED). */
 size_t bd_base_gemm_fp8_n_workspace_bytes(int64_t T, int64_t d_in, int32_t n_mats,
                                           const int64_t* d_outs);
 bd_status bd_base_gemm_fp8_n(const uint8_t* x_codes, const uint8_t* x_scales, int64_t T,
