@@ -880,7 +880,7 @@ __device__ __forceinline__ void put1(uint16_t* y, int64_t i, float v) { y[i] = f
 
 template <typename YT>
 __global__ void __launch_bounds__(256)
-k_mx4_reduce(const GemmMats gm, int T, int S) {
+k_sum_parts(const GemmMats gm, int T, int S) {
     typedef f32x4 f32x4_a4 __attribute__((aligned(4)));  // (a part starts at any float)
     const int mi = (int)blockIdx.y;
     const int64_t n = (int64_t)T * gm.N[mi];
@@ -965,8 +965,8 @@ Mx4Plan plan_mx4(bool x4, int64_t T, int64_t d_in, const int64_t* d_outs, int n,
 hipError_t launch_sum_parts(const GemmMats& gm, int64_t T, int64_t nmax, int S, int ydtype, hipStream_t s) {
     const int64_t nb = (T * nmax / 4 + 255) / 256;
     const dim3 grid((unsigned)(nb < 1 ? 1 : nb < 2048 ? nb : 2048), (unsigned)gm.n), block(256);
-    if (ydtype == BD_BF16) k_mx4_reduce<uint16_t><<<grid, block, 0, s>>>(gm, (int)T, S);
-    else k_mx4_reduce<float><<<grid, block, 0, s>>>(gm, (int)T, S);
+    if (ydtype == BD_BF16) k_sum_parts<uint16_t><<<grid, block, 0, s>>>(gm, (int)T, S);
+    else k_sum_parts<float><<<grid, block, 0, s>>>(gm, (int)T, S);
     return hipGetLastError();
 }
 
