@@ -65,3 +65,36 @@ def test_blocks_that_are_not_finite(T):
     inf[0, 3] = float("inf")
     (y,) = B.base_gemm_fp8((x, xs), [(w, inf)])
     assert not torch.isfinite(y[:, :128]).any() and torch.equal(y[:, 128:], want[:, 128:])
+
+
+CODES = torch.arange(256, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 256, 700])
+def test_every_code(T):
+    """Each of the 256 codes, as a weight under tokens of 1 and as a token over weights of 1, in the
+    column that its index picks: finite ones exactly (subnormals and both zeros too), the two NaN codes
+    in their own outputs alone."""
+    cols, rows = 320, 256
+    nb, ld = (cols + 127) // 128, B.bd_fp8_scale_stride(cols)
+    one = torch.ones((), dtype=torch.float32).to(E4M3).view(torch.uint8)
+    xs = torch.zeros(T, ld, dtype=torch.uint8, device=DEV)
+    xs[:, :nb] = 127
+    w = torch.zeros(rows, cols, dtype=torch.uint8)
+    w[CODES.long(), (7 * CODES.long()) % cols] = CODES
+    x = one.expand(T, cols).contiguous()
+    ws = torch.ones((rows + 127) // 128, nb, device=DEV)
+    val = CODES.view(E4M3).float().to(DEV)
+    (y,) = B.base_gemm_fp8((x.view(E4M3).to(DEV), xs), [(w.view(E4M3).to(DEV), ws)])
+    assert torch.equal(torch.nan_to_num(y, nan=1e9), torch.nan_to_num(val, nan=1e9).expand(T, rows))
+    t = torch.arange(T)
+    x = torch.zeros(T, cols, dtype=torch.uint8)
+    x[t, (11 * t) % cols] = CODES[t % 256]
+    (y,) = B.base_gemm_fp8((x.view(E4M3).to(DEV), xs), [(one.expand(rows, cols).contiguous().view(E4M3).to(DEV), ws)])
+    assert torch.equal(torch.nan_to_num(y, nan=1e9), torch.nan_to_num(val[t % 256], nan=1e9)[:, None].expand(T, rows))
+    # the apply's base part (user -1), in one launch up to 16 tokens
+    p, ids = B.params("matrix"), torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    signs = torch.zeros(1, rows, cols // 64, dtype=torch.int64, device=DEV)
+    a = B.apply_fp8(torch.zeros(T, cols, dtype=torch.bfloat16, device=DEV), one.expand(rows, cols).contiguous().view(E4M3).to(DEV), ws,
+                    signs, torch.ones(1, 1, device=DEV), p, ids, xq=(x.view(E4M3).to(DEV), xs), check=True)
+    assert torch.equal(torch.nan_to_num(a, nan=1e9), torch.nan_to_num(y, nan=1e9))
