@@ -489,9 +489,9 @@ k_fp8_rows(const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const 
 // 128 of them widen; the same mix run from registers alone, without LDS, reached 1600 TFLOP/s, a
 // library's bf16 product 1391 to 1458.  8192 tokens on 14336 x 4096, fp32 out: 830 to 875 us,
 // 1100 to 1160 TFLOP/s; 780 where the copies bring nothing from memory, 720 with the codes taken
-// as they are (no widening).  Less ordering between the instructions, chains of one tile, or two
-// blocks of four waves a CU: within 2%.  Wave tiles of 128 x 64 leave no registers for the
-// widened operands.
+// as they are (no widening).  Less ordering between the instructions or chains of one tile: within
+// 2%; 128 x 128 on four waves, two blocks a CU: 960.  Wave tiles of 128 x 64 leave no registers for
+// the widened operands.
 // Middling batches: 1144 tokens on 5120 x 17408, 240 tiles of 256 x 192 in two K parts on 256
 // CUs, 183 us (1110 TFLOP/s; as many of 128 x 192 over all of K 192, 160 of them without
 // widening): 6 tiles of 192 tokens cover 1144 where 9 of 128 or 5 of 256 would leave a second
